@@ -20,6 +20,7 @@ SPARK_ERR_UNSUPPORTED = 2
 SPARK_ERR_CUDA = 3
 SPARK_ERR_TIMEOUT = 4
 SPARK_ERR_WORKSPACE = 5
+SPARK_ERR_PAGES = 6
 SPARK_F32 = 0
 SPARK_BF16 = 1
 SPARK_F_DEGENERATE = 0
@@ -30,12 +31,16 @@ SPARK_OP_DECODE = 1
 SPARK_OP_SNAPKV = 2
 SPARK_OP_THINK = 3
 SPARK_OP_TOPP = 4
+SPARK_KV8_E4M3 = 0
+SPARK_KV8_I8 = 1
 
 EXPORTS = ("spark_lambda_to_T", "spark_cache_sizes", "spark_cache_bytes", "spark_workspace_bytes",
            "spark_prune", "spark_prune_noalloc", "spark_prune_grouped", "spark_group_budget", "spark_prune_values", "spark_prune_think", "spark_prune_topp", "spark_decode_attn",
            "spark_decode_attn_topp", "spark_topp_offsets_bytes", "spark_topp_vals_used",
            "spark_decode_attn_kv", "spark_workspace_bytes_kv", "spark_selftest_wait_timeout", "spark_tail_append", "spark_device_status",
-           "spark_status_str", "spark_snapkv_evict", "spark_snapkv_evict_rows", "spark_pyramid_keep")
+           "spark_status_str", "spark_snapkv_evict", "spark_snapkv_evict_rows", "spark_pyramid_keep",
+           "spark_kv8_sizes", "spark_pages_extend", "spark_pages_trim", "spark_kv8_append",
+           "spark_decode_attn_kv8", "spark_workspace_bytes_kv8")
 
 
 class SparkError(RuntimeError):
@@ -49,6 +54,12 @@ class spark_kcache(ctypes.Structure):
                 ("T", ctypes.c_int), ("dtype", ctypes.c_int), ("mask", ctypes.c_void_p),
                 ("vals", ctypes.c_void_p), ("qn", ctypes.c_void_p), ("stats", ctypes.c_void_p),
                 ("goff", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class spark_kv8cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("page", ctypes.c_int), ("D", ctypes.c_int),
+                ("type", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +121,19 @@ def lib():
         L.spark_pyramid_keep.restype = I
         L.spark_tail_append.argtypes = [P, P, P, P, I, I, I, I, I, I, P]
         L.spark_tail_append.restype = I
+        KV8 = ctypes.POINTER(spark_kv8cache)
+        L.spark_kv8_sizes.argtypes = [I, I, I, I, ctypes.POINTER(Z)]
+        L.spark_kv8_sizes.restype = Z
+        L.spark_pages_extend.argtypes = [P, P, I, I, P, I, P, P, I, I, P, P, P, P, Z, P]
+        L.spark_pages_extend.restype = I
+        L.spark_pages_trim.argtypes = [P, P, I, I, P, I, P, P, I, P, P, P, Z, P]
+        L.spark_pages_trim.restype = I
+        L.spark_kv8_append.argtypes = [P, P, I, I, I, P, KV8, P, Z, P]
+        L.spark_kv8_append.restype = I
+        L.spark_decode_attn_kv8.argtypes = [P, I, KV8, P, I, P, P, I, I, I, P, P, Z, P]
+        L.spark_decode_attn_kv8.restype = I
+        L.spark_workspace_bytes_kv8.argtypes = [I, I, I, I]
+        L.spark_workspace_bytes_kv8.restype = Z
         L.spark_device_status.argtypes = [P, ctypes.POINTER(I), I, P]
         L.spark_device_status.restype = I
         L.spark_status_str.argtypes = [I]
@@ -371,6 +395,143 @@ def spark_tail_append(k_new, v_new, k_tail, v_tail, B, Hkv, D, tail_cap, slot, s
     rc = lib().spark_tail_append(_ptr(k_new), _ptr(v_new), _ptr(k_tail), _ptr(v_tail), B, Hkv, D,
                                  tail_cap, slot, _dtype_code(k_new.dtype), _stream(stream))
     _check(rc, "spark_tail_append")
+
+
+# ------------------------------------------------------ paged 8-bit cache
+@dataclass
+class KV8Cache:
+    """Device tensors of the paged 8-bit cache (layout of include/spark.h)."""
+    n_pages: int
+    Hkv: int
+    page: int             # tokens per page: 16, 32, 64 or 128
+    D: int
+    type: int             # SPARK_KV8_E4M3 or SPARK_KV8_I8
+    k: torch.Tensor       # uint8 [n_pages, Hkv, page, D]
+    v: torch.Tensor       # uint8 [n_pages, Hkv, page, D]
+    k_scale: torch.Tensor  # fp32 [n_pages, Hkv]
+    v_scale: torch.Tensor  # fp32 [n_pages, Hkv]
+
+    def __post_init__(self):
+        codes, scales = (self.n_pages, self.Hkv, self.page, self.D), (self.n_pages, self.Hkv)
+        for name, t, shape, dt in (("k", self.k, codes, torch.uint8), ("v", self.v, codes, torch.uint8),
+                                   ("k_scale", self.k_scale, scales, torch.float32),
+                                   ("v_scale", self.v_scale, scales, torch.float32)):
+            _need(t, name, dt, shape, self.k.device)
+        self._struct = spark_kv8cache(self.n_pages, self.Hkv, self.page, self.D, self.type, _ptr(self.k),
+                                      _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale))
+
+    @staticmethod
+    def empty(n_pages, Hkv, page, type=SPARK_KV8_E4M3, D=128, device="cuda") -> "KV8Cache":
+        codes = [torch.empty((n_pages, Hkv, page, D), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.empty((n_pages, Hkv), dtype=torch.float32, device=device) for _ in range(2)]
+        return KV8Cache(n_pages, Hkv, page, D, type, *codes, *scales)
+
+    def struct(self) -> spark_kv8cache:
+        return self._struct
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+
+def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """The library sees bare pointers: a tensor of another type, shape, layout
+    or device than the call needs is refused here."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} needed, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} needed, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {device}")
+
+
+def _launch_stream(device, stream) -> int | None:
+    """The stream to launch on; kernels start on the current device, so the tensors must be there."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: they must be on the current CUDA device")
+    return _stream(stream)
+
+
+def spark_kv8_sizes(n_pages: int, Hkv: int, page: int, D: int = 128) -> tuple[int, list[int]]:
+    sizes = (ctypes.c_size_t * 4)()
+    total = lib().spark_kv8_sizes(n_pages, Hkv, page, D, sizes)
+    return int(total), [int(x) for x in sizes]
+
+
+def spark_pages_extend(lens: torch.Tensor, n_new: torch.Tensor, page: int, pool: torch.Tensor, taken: torch.Tensor,
+                       table: torch.Tensor, slots: torch.Tensor, lens_out: torch.Tensor, taken_out: torch.Tensor,
+                       ws: torch.Tensor, stream=None) -> None:
+    """Pages for each row's n_new tokens (table [B, cap] and taken_out) and
+    their slots [B, n_cap]; lens_out / taken_out may be lens / taken."""
+    B, dev, i32 = lens.shape[0], lens.device, torch.int32
+    cap, n_cap, n_pages = table.shape[-1], slots.shape[-1], pool.shape[0]
+    for t, name, shape in ((lens, "lens", (B,)), (n_new, "n_new", (B,)), (pool, "pool", (n_pages,)),
+                           (taken, "taken", (1,)), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
+                           (lens_out, "lens_out", (B,)), (taken_out, "taken_out", (1,))):
+        _need(t, name, i32, shape, dev)
+    rc = lib().spark_pages_extend(lens.data_ptr(), n_new.data_ptr(), B, page, pool.data_ptr(), n_pages,
+                                  taken.data_ptr(), table.data_ptr(), cap, n_cap, slots.data_ptr(),
+                                  lens_out.data_ptr(), taken_out.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _launch_stream(dev, stream))
+    _check(rc, "spark_pages_extend")
+
+
+def spark_pages_trim(lens: torch.Tensor, keep: torch.Tensor, page: int, pool: torch.Tensor, taken: torch.Tensor,
+                     table: torch.Tensor, lens_out: torch.Tensor, taken_out: torch.Tensor, ws: torch.Tensor,
+                     stream=None) -> None:
+    """Cut each row to its first keep tokens and give the pages behind them
+    back to the pool; lens_out / taken_out may be lens / taken."""
+    B, dev, i32 = lens.shape[0], lens.device, torch.int32
+    cap, n_pages = table.shape[-1], pool.shape[0]
+    for t, name, shape in ((lens, "lens", (B,)), (keep, "keep", (B,)), (pool, "pool", (n_pages,)),
+                           (taken, "taken", (1,)), (table, "table", (B, cap)), (lens_out, "lens_out", (B,)),
+                           (taken_out, "taken_out", (1,))):
+        _need(t, name, i32, shape, dev)
+    rc = lib().spark_pages_trim(lens.data_ptr(), keep.data_ptr(), B, page, pool.data_ptr(), n_pages,
+                                taken.data_ptr(), table.data_ptr(), cap, lens_out.data_ptr(), taken_out.data_ptr(),
+                                ws.data_ptr(), ws.numel() * ws.element_size(), _launch_stream(dev, stream))
+    _check(rc, "spark_pages_trim")
+
+
+def spark_kv8_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, kc: KV8Cache, ws: torch.Tensor,
+                     stream=None) -> None:
+    """Write k_new, v_new [B, Hkv, n_cap, D] into the slots [B, n_cap] in 8
+    bits ([B, Hkv, D] with n_cap = 1)."""
+    B, n_cap = slots.shape
+    dev = kc.k.device
+    shape = (B, kc.Hkv, kc.D) if k_new.dim() == 3 and n_cap == 1 else (B, kc.Hkv, n_cap, kc.D)
+    _need(k_new, "k_new", k_new.dtype, shape, dev)
+    _need(v_new, "v_new", k_new.dtype, shape, dev)
+    _need(slots, "slots", torch.int32, (B, n_cap), dev)
+    rc = lib().spark_kv8_append(k_new.data_ptr(), v_new.data_ptr(), B, n_cap, _dtype_code(k_new.dtype),
+                                slots.data_ptr(), ctypes.byref(kc.struct()), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _launch_stream(dev, stream))
+    _check(rc, "spark_kv8_append")
+
+
+def spark_decode_attn_kv8(q: torch.Tensor, kc: KV8Cache, table: torch.Tensor, lens: torch.Tensor, G: int,
+                          out: torch.Tensor, ws: torch.Tensor, n_new: torch.Tensor = None, stream=None) -> None:
+    """Attention of q [B, Hkv*G, n_q, D] (or [B, Hkv*G, D]), each row's newest
+    tokens, over its pages; out fp32, shaped like q."""
+    B, cap = table.shape
+    dev = kc.k.device
+    n_q = q.shape[2] if q.dim() == 4 else 1
+    shape = (B, kc.Hkv * G, n_q, kc.D) if q.dim() == 4 else (B, kc.Hkv * G, kc.D)
+    _need(q, "q", q.dtype, shape, dev)
+    _need(out, "out", torch.float32, shape, dev)
+    _need(table, "table", torch.int32, (B, cap), dev)
+    _need(lens, "lens", torch.int32, (B,), dev)
+    if n_new is not None:
+        _need(n_new, "n_new", torch.int32, (B,), dev)
+    rc = lib().spark_decode_attn_kv8(q.data_ptr(), _dtype_code(q.dtype), ctypes.byref(kc.struct()),
+                                     table.data_ptr(), cap, lens.data_ptr(), _ptr(n_new), B, G, n_q, out.data_ptr(),
+                                     ws.data_ptr(), ws.numel() * ws.element_size(), _launch_stream(dev, stream))
+    _check(rc, "spark_decode_attn_kv8")
+
+
+def spark_workspace_bytes_kv8(B: int, Hkv: int, G: int, n_q: int = 1) -> int:
+    return int(lib().spark_workspace_bytes_kv8(B, Hkv, G, n_q))
 
 
 def spark_device_status(ws: torch.Tensor, clear: bool = False, stream=None) -> int:

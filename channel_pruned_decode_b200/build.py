@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspark.so")
 
-SOURCES = ["api.cu", "prune.cu", "decode.cu", "snapkv.cu", "think.cu"]
+SOURCES = ["api.cu", "prune.cu", "decode.cu", "snapkv.cu", "think.cu", "pages.cu", "kv8.cu", "attn_kv8.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -38,7 +38,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ into libspark.so (exported: the C ABI of
     include/spark.h only).  Returns the library path."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(CSRC, "spark_internal.cuh"), os.path.join(INCLUDE, "spark.h")]
+    deps = srcs + [os.path.join(CSRC, "spark_internal.cuh"), os.path.join(CSRC, "kv8.cuh"), os.path.join(INCLUDE, "spark.h")]
     if not force and not _stale(LIB, deps):
         return LIB
     nvcc = _nvcc()

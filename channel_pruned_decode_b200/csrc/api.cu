@@ -26,6 +26,19 @@ cudaError_t launch_snapkv(const void *k, const void *v, const void *q_obs, long 
 
 size_t snapkv_partials_bytes(long BH);
 
+cudaError_t launch_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
+                                int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
+                                int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *ws, cudaStream_t st);
+cudaError_t launch_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool, int n_pages,
+                              const int32_t *taken, const int32_t *table, int table_cap, int32_t *lens_out,
+                              int32_t *taken_out, void *ws, cudaStream_t st);
+cudaError_t launch_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype,
+                              const int32_t *slots, const spark_kv8cache &kc, void *ws, cudaStream_t st);
+cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, const int32_t *table, int table_cap,
+                            const int32_t *lens, const int32_t *n_new, int B, int G, int n_q, float *out, void *ws,
+                            int num_sms, cudaStream_t st);
+size_t attn_kv8_workspace(int B, int Hkv, int rows, int num_sms);
+
 // scores (fp32) and pooled keys (u32) per prefix token, then the per-split
 // softmax partials
 static size_t snapkv_workspace(long BH, int S, int W) {
@@ -386,6 +399,117 @@ int spark_tail_append(const void *k_new, const void *v_new, void *k_tail, void *
     return cudaGetLastError() == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
+size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t sizes[4]) {
+    if (n_pages < 0 || Hkv < 0 || D != kD || !kv8_page_ok(page)) return 0;
+    if ((double)n_pages * Hkv * page > 2147483647.0) return 0;
+    const size_t PH = (size_t)n_pages * Hkv;
+    const size_t sz[4] = {PH * page * D, PH * page * D, PH * sizeof(float), PH * sizeof(float)};
+    size_t total = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (sizes) sizes[i] = sz[i];
+        total += round256(sz[i]);
+    }
+    return total;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// a != b may share no byte (the same pointer twice is one array, updated in place)
+static bool overlap(const void *a, const void *b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && x < y + bytes && y < x + bytes;
+}
+
+// checks that spark_pages_extend and spark_pages_trim share
+static int check_pages(const int32_t *lens, const int32_t *n, int B, int page, const int32_t *pool, int n_pages,
+                       const int32_t *taken, const int32_t *table, int table_cap, const int32_t *lens_out,
+                       const int32_t *taken_out) {
+    if (B < 0 || n_pages < 0 || table_cap < 0) return SPARK_ERR_ARG;
+    if (!kv8_page_ok(page)) return SPARK_ERR_UNSUPPORTED;
+    if ((double)B * table_cap + n_pages > 2147483647.0 || (double)table_cap * page > 2147483647.0)
+        return SPARK_ERR_UNSUPPORTED;
+    if (B == 0) return SPARK_OK;
+    if (!lens || !n || !taken || !lens_out || !taken_out || (n_pages > 0 && !pool) || (table_cap > 0 && !table))
+        return SPARK_ERR_ARG;
+    if (!aligned4(lens) || !aligned4(n) || !aligned4(taken) || !aligned4(lens_out) || !aligned4(taken_out) ||
+        !aligned4(pool) || !aligned4(table))
+        return SPARK_ERR_ARG;
+    if (overlap(lens, lens_out, (size_t)B * 4) || n == lens_out || overlap(n, lens_out, (size_t)B * 4))
+        return SPARK_ERR_ARG;
+    return SPARK_OK;
+}
+
+int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool, int n_pages,
+                       const int32_t *taken, int32_t *table, int table_cap, int n_cap, int32_t *slots,
+                       int32_t *lens_out, int32_t *taken_out, void *workspace, size_t ws_bytes, void *stream) {
+    const int rc = check_pages(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, lens_out, taken_out);
+    if (rc != SPARK_OK) return rc;
+    if (n_cap < 0) return SPARK_ERR_ARG;
+    if ((double)B * (n_cap / 2048 + 1) > 2147483647.0) return SPARK_ERR_UNSUPPORTED;  // CTAs
+    if (B == 0) return SPARK_OK;
+    if (n_cap > 0 && (!slots || !aligned16(slots))) return SPARK_ERR_ARG;
+    if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;
+    cudaError_t e = launch_pages_extend(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, n_cap, slots,
+                                        lens_out, taken_out, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
+int spark_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool, int n_pages,
+                     const int32_t *taken, const int32_t *table, int table_cap, int32_t *lens_out,
+                     int32_t *taken_out, void *workspace, size_t ws_bytes, void *stream) {
+    const int rc = check_pages(lens, keep, B, page, pool, n_pages, taken, table, table_cap, lens_out, taken_out);
+    if (rc != SPARK_OK) return rc;
+    if (B == 0) return SPARK_OK;
+    if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;
+    cudaError_t e = launch_pages_trim(lens, keep, B, page, pool, n_pages, taken, table, table_cap, lens_out,
+                                      taken_out, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
+int spark_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype, const int32_t *slots,
+                     const spark_kv8cache *kc, void *workspace, size_t ws_bytes, void *stream) {
+    const int rc = check_kv8(kc);
+    if (rc != SPARK_OK) return rc;
+    if (B < 0 || n_cap < 0 || elem_size(dtype) == 0) return SPARK_ERR_ARG;
+    // 32-bit counts of (row, page-sized piece, head, key or value) and of slots
+    if ((double)B * kc->Hkv * ((n_cap + 15) / 16) * 2 > 2147483647.0 || (double)B * n_cap > 2147483647.0)
+        return SPARK_ERR_UNSUPPORTED;
+    if ((long)B * kc->Hkv == 0 || n_cap == 0) return SPARK_OK;
+    if (!k_new || !v_new || !slots || !aligned16(k_new) || !aligned16(v_new) || !aligned4(slots))
+        return SPARK_ERR_ARG;
+    if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;
+    cudaError_t e = launch_kv8_append(k_new, v_new, B, n_cap, dtype, slots, *kc, workspace,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
+size_t spark_workspace_bytes_kv8(int B, int Hkv, int G, int n_q) {
+    if (B < 0 || Hkv < 0 || G < 1 || n_q < 1 || (long)G * n_q > kKv8MaxRows) return 0;
+    if ((double)B * Hkv * kKv8MaxRows > 2147483647.0) return 0;
+    return round256(attn_kv8_workspace(B, Hkv, G * n_q, num_sms()));
+}
+
+int spark_decode_attn_kv8(const void *q, int dtype, const spark_kv8cache *kc, const int32_t *table, int table_cap,
+                          const int32_t *lens, const int32_t *n_new, int B, int G, int n_q, float *out,
+                          void *workspace, size_t ws_bytes, void *stream) {
+    const int rc = check_kv8(kc);
+    if (rc != SPARK_OK) return rc;
+    if (B < 0 || table_cap < 0 || G < 1 || n_q < 1 || elem_size(dtype) == 0) return SPARK_ERR_ARG;
+    if ((long)G * n_q > kKv8MaxRows) return SPARK_ERR_UNSUPPORTED;
+    if ((double)table_cap * kc->page > 2147483647.0 || (double)B * kc->Hkv * kKv8MaxRows > 2147483647.0)
+        return SPARK_ERR_UNSUPPORTED;
+    if ((long)B * kc->Hkv == 0) return SPARK_OK;
+    if (!q || !aligned16(q) || !out || !aligned16(out) || !lens || !aligned4(lens) || !aligned4(n_new))
+        return SPARK_ERR_ARG;
+    if (table_cap > 0 && (!table || !aligned4(table))) return SPARK_ERR_ARG;
+    if (!workspace || !aligned16(workspace)) return SPARK_ERR_WORKSPACE;
+    const int sms = num_sms();
+    if (ws_bytes < attn_kv8_workspace(B, kc->Hkv, G * n_q, sms)) return SPARK_ERR_WORKSPACE;
+    cudaError_t e = launch_attn_kv8(q, dtype, *kc, table, table_cap, lens, n_new, B, G, n_q, out, workspace, sms,
+                                    static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
 int spark_selftest_wait_timeout(void *workspace, int limit_us, void *stream) {
     if (!workspace || !aligned16(workspace)) return SPARK_ERR_WORKSPACE;
     if (limit_us < 1 || limit_us > 1000000) return SPARK_ERR_ARG;
@@ -401,7 +525,10 @@ int spark_device_status(void *workspace, int *status, int clear, void *stream) {
     if (cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess)
         return SPARK_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return SPARK_ERR_CUDA;
-    *status = (word & kDevTimeout) ? SPARK_ERR_TIMEOUT : ((word & kDevBadArg) ? SPARK_ERR_ARG : SPARK_OK);
+    *status = (word & kDevTimeout)   ? SPARK_ERR_TIMEOUT
+              : (word & kDevNoPages) ? SPARK_ERR_PAGES
+              : (word & kDevBadArg)  ? SPARK_ERR_ARG
+                                     : SPARK_OK;
     if (clear && word) {
         if (cudaMemsetAsync(workspace, 0, sizeof(word), st) != cudaSuccess) return SPARK_ERR_CUDA;
         if (cudaStreamSynchronize(st) != cudaSuccess) return SPARK_ERR_CUDA;
@@ -417,6 +544,7 @@ const char *spark_status_str(int status) {
     case SPARK_ERR_CUDA: return "CUDA error";
     case SPARK_ERR_TIMEOUT: return "device-side wait timed out";
     case SPARK_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case SPARK_ERR_PAGES: return "page pool exhausted";
     default: return "unknown status";
     }
 }

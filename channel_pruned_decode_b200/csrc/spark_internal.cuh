@@ -16,6 +16,7 @@ constexpr int kMaskWords = kD / 32;   // 128-bit channel mask per token
 constexpr int kWsHeader = 256;        // status word + padding at workspace start
 constexpr uint32_t kDevTimeout = 1u;  // status bit: a bounded wait ran out
 constexpr uint32_t kDevBadArg = 2u;   // status bit: a device-side length or budget was out of range
+constexpr uint32_t kDevNoPages = 4u;  // status bit: the page pool ran out
 
 // ------------------------------------------------------- argument checks
 inline int elem_size(int dtype) { return dtype == SPARK_F32 ? 4 : (dtype == SPARK_BF16 ? 2 : 0); }
@@ -168,6 +169,25 @@ DecodeGeom decode_geometry(long BH, int S, int T, int Tv, int es, int G, int num
 inline size_t decode_workspace(long BH, const DecodeGeom &g, int G) {
     return kWsHeader + (size_t)BH * g.units * G * (kD + 2) * sizeof(float);
 }
+
+// ------------------------------------------------------- paged 8-bit cache
+// rows of 128 codes are addressed with 32 bits: [n_pages][Hkv][page] of them
+inline bool kv8_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+inline int check_kv8(const spark_kv8cache *kc) {
+    if (!kc) return SPARK_ERR_ARG;
+    if (kc->n_pages < 0 || kc->Hkv < 0) return SPARK_ERR_ARG;
+    if (kc->type != SPARK_KV8_E4M3 && kc->type != SPARK_KV8_I8) return SPARK_ERR_ARG;
+    if (kc->D != kD || !kv8_page_ok(kc->page)) return SPARK_ERR_UNSUPPORTED;
+    if ((double)kc->n_pages * kc->Hkv * kc->page > 2147483647.0) return SPARK_ERR_UNSUPPORTED;
+    if ((long)kc->n_pages * kc->Hkv == 0) return SPARK_OK;
+    if (!kc->k || !kc->v || !kc->k_scale || !kc->v_scale) return SPARK_ERR_ARG;
+    if (!aligned16(kc->k) || !aligned16(kc->v) || !aligned16(kc->k_scale) || !aligned16(kc->v_scale))
+        return SPARK_ERR_ARG;
+    return SPARK_OK;
+}
+
+constexpr int kKv8MaxRows = 64;  // query rows per kv head (G * n_q) of one call
 
 // ------------------------------------------------------- element access
 template <typename E> struct Elem;

@@ -55,7 +55,8 @@ typedef enum {
     SPARK_ERR_UNSUPPORTED = 2,  /* valid request the library does not run     */
     SPARK_ERR_CUDA = 3,         /* a CUDA call failed (launch, attribute)     */
     SPARK_ERR_TIMEOUT = 4,      /* device-side bounded wait ran out           */
-    SPARK_ERR_WORKSPACE = 5     /* workspace NULL, misaligned or too small    */
+    SPARK_ERR_WORKSPACE = 5,    /* workspace NULL, misaligned or too small    */
+    SPARK_ERR_PAGES = 6         /* the page pool ran out (device status)      */
 } spark_status;
 
 typedef enum { SPARK_F32 = 0, SPARK_BF16 = 1 } spark_dtype;
@@ -435,10 +436,145 @@ SPARK_API int spark_tail_append(const void *k_new, const void *v_new, void *k_ta
                       void *v_tail, int B, int Hkv, int D, int tail_cap,
                       int slot, int dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache: page tables and slot maps built on the GPU,
+ * the write into the cache and the attention that reads it.  Not part of the
+ * SparK method ([A] calls SparK orthogonal to quantisation and gives no
+ * scheme): the formats and rules below are the library's.
+ *
+ * One serving step is spark_pages_extend (room for the new tokens),
+ * spark_kv8_append (their keys and values), spark_decode_attn_kv8, and
+ * spark_pages_trim for tokens that are taken back or requests that ended.
+ * The lengths, tables and counts stay on the GPU, so a step can be captured
+ * in a CUDA graph and replayed.
+ */
+
+typedef enum {
+    SPARK_KV8_E4M3 = 0,   /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest 448 */
+    SPARK_KV8_I8 = 1      /* whole numbers -127 .. 127 */
+} spark_kv8_type;
+
+/*
+ * The pool of pages.  A page holds `page` tokens of every kv head:
+ *   k, v              one byte per value, [n_pages][Hkv][page][D]
+ *   k_scale, v_scale  fp32 [n_pages][Hkv]; value = code * scale.
+ * page is 16, 32, 64 or 128; D must be 128; n_pages * Hkv * page < 2^31.
+ * Device memory owned by the caller; it needs no initialisation.
+ */
+typedef struct spark_kv8cache {
+    int n_pages, Hkv, page, D, type;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} spark_kv8cache;
+
+/* Byte sizes of the four regions {k, v, k_scale, v_scale} (written to
+ * sizes[0..3] unless NULL) and their total when packed back to back at
+ * 256-byte aligned offsets (the return value).  0 on bad arguments. */
+SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t sizes[4]);
+
+/*
+ * Give rows the pages that their new tokens need, and map each new token to
+ * its slot.
+ *   lens    int32 [B]  tokens that each row holds
+ *   n_new   int32 [B]  tokens that it gets now, at most n_cap
+ *   pool    int32 [n_pages]  page numbers; the free ones are pool[taken ..]
+ *   taken   int32 [1]  how many of the pool's entries are in use
+ *   table   int32 [B][table_cap]  pages of each row in token order; entries
+ *           of its new pages are written, all others are left as they are
+ *   slots   int32 [B][n_cap], out: slot of new token j (token lens[b] + j of
+ *           the row) = page number * page + place in the page; -1 past n_new
+ *   lens_out, taken_out  int32 [B], [1], out: the lengths and the count
+ *           afterwards.  They may be lens and taken themselves.
+ * Rows are served in order: row b's new pages are the next entries of the
+ * pool.  When the pool runs out, the tokens without a page get slot -1, the
+ * table entries without one get -1, lens_out counts only the tokens that
+ * have one, and SPARK_ERR_PAGES is raised in the device status word.
+ * Lengths out of range (negative, n_new > n_cap, more tokens than table_cap
+ * pages hold, taken outside [0, n_pages], a page number outside the pool)
+ * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
+ * Requires B * table_cap + n_pages < 2^31 and table_cap * page < 2^31.
+ * Workspace: 256 bytes, zero before first use, not shared with a call that
+ * may run at the same time (this holds for every workspace of the library).
+ * B = 0 launches nothing and leaves taken_out as it is.
+ */
+SPARK_API int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
+                                 int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
+                                 int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *workspace,
+                                 size_t ws_bytes, void *stream);
+
+/*
+ * Cut rows to their first keep[b] tokens (0: the request has ended; keep >=
+ * lens: the row is left as it is) and give the pages behind them back.
+ *   keep    int32 [B], not negative
+ * The pages of all rows, in row and token order, become
+ * pool[taken - their number ..] and taken goes down by their number.  Table
+ * entries are left as they are.  lens_out and taken_out may be lens and
+ * taken.  Pages belong to one row: a page that two rows list is given back
+ * twice.  Bad lengths or page numbers raise SPARK_ERR_ARG in the device
+ * status word (a bad page number is given back as -1, which
+ * spark_pages_extend hands on as "no page").  Workspace as above.
+ */
+SPARK_API int spark_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool,
+                               int n_pages, const int32_t *taken, const int32_t *table, int table_cap,
+                               int32_t *lens_out, int32_t *taken_out, void *workspace, size_t ws_bytes,
+                               void *stream);
+
+/*
+ * Write new keys and values into their slots in 8 bits.
+ *   k_new, v_new  [B][Hkv][n_cap][D] dtype (SPARK_F32 or SPARK_BF16)
+ *   slots         int32 [B][n_cap] as written by spark_pages_extend; a
+ *                 negative slot's token is not written
+ * Per kv head, the new tokens that lie one after another in a page share a
+ * scale: with a = their largest finite |x| and M = 448 (e4m3) or 127 (int8),
+ * the scale is 2^E for the smallest E in [-126, 120] with a <= M 2^E.  Where
+ * they start inside a page (place o > 0) the page's scale only grows: 2^E is
+ * the larger of that and the page's own, and when it grew the codes of
+ * places 0 .. o-1 are rounded again to the new scale.  A code is x / 2^E
+ * rounded to nearest even, which is exact arithmetic up to that one
+ * rounding; larger values and infinities become the largest code, NaN stays
+ * NaN (e4m3) or becomes 0 (int8).
+ * The tokens of a page must stand one after another in one row of slots, in
+ * ascending order, as spark_pages_extend writes them; a page that appears in
+ * several places of one call gets unspecified codes and scales.  A slot past
+ * the pool is not written and raises SPARK_ERR_ARG in the device status
+ * word.  Workspace: 256 bytes, as above.
+ */
+SPARK_API int spark_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype,
+                               const int32_t *slots, const spark_kv8cache *kc, void *workspace, size_t ws_bytes,
+                               void *stream);
+
+/*
+ * Attention of the newest tokens of each row over its pages.
+ *   q       [B][Hkv*G][n_q][D] dtype   queries (n_q = 1: one decode step)
+ *   table   int32 [B][table_cap]       pages of each row in token order
+ *   lens    int32 [B]                  tokens of each row, the new ones among them
+ *   n_new   int32 [B] or NULL          how many of the n_q queries row b has
+ *                                      (NULL: all); query i is token
+ *                                      lens[b] - n_new[b] + i of the row
+ *   out     [B][Hkv*G][n_q][D] fp32
+ * Query i sees the tokens up to its own:
+ *   out = softmax(q . K^T / sqrt(D)) V,  K, V = code * scale,
+ * with fp32 products' sums and statistics; a query that sees no token gets
+ * zeros, and the rows of queries i >= n_new[b] are left as they are.  What
+ * the pages hold past lens[b], and table entries past it, is never used.
+ * Requires 1 <= G * n_q <= 64.  Lengths out of range (lens past table_cap
+ * pages, n_new outside [0, n_q]) are clamped and page numbers outside the
+ * pool make their tokens unseen; both raise SPARK_ERR_ARG in the device
+ * status word.  Workspace: spark_workspace_bytes_kv8(B, Hkv, G, n_q).
+ * Results do not depend on timing: the same call gives the same bits.
+ */
+SPARK_API int spark_decode_attn_kv8(const void *q, int dtype, const spark_kv8cache *kc, const int32_t *table,
+                                    int table_cap, const int32_t *lens, const int32_t *n_new, int B, int G, int n_q,
+                                    float *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of spark_decode_attn_kv8; depends on the current device's
+ * SM count.  0 on bad arguments. */
+SPARK_API size_t spark_workspace_bytes_kv8(int B, int Hkv, int G, int n_q);
+
 /* Synchronise `stream`, read the device status word at the start of
  * `workspace` into *status (SPARK_OK, SPARK_ERR_TIMEOUT when a bounded wait
- * ran out, SPARK_ERR_ARG when a device-side length or budget was out of
- * range) and, when clear != 0, reset it to zero.  Returns SPARK_ERR_CUDA if
+ * ran out, SPARK_ERR_PAGES when a page pool ran out, SPARK_ERR_ARG when a
+ * device-side length, budget, slot or page number was out of range) and, when clear != 0, reset it to zero.  Returns SPARK_ERR_CUDA if
  * a copy fails. */
 SPARK_API int spark_device_status(void *workspace, int *status, int clear, void *stream);
 
