@@ -325,6 +325,31 @@ def test_attn_nan_reaches_only_those_who_see_it():
     assert torch.equal(out[1, :4, :, 10:], clean[1, :4, :, 10:])
 
 
+@pytest.mark.parametrize("G,n_q", [(2, 2), (4, 4), (3, 20), (8, 8)])
+def test_attn_nan_in_a_place_that_some_queries_do_not_see(G, n_q):
+    lens, page = [100 + n_q], 16
+    kc, table = _context(lens, 2, page, SPARK_KV8_E4M3, 4)
+    q = _values(_gen(5), (1, 2 * G, n_q, D), torch.bfloat16)
+    clean, _ = _attend(q, kc, table, lens, G)
+    first = {}  # channel -> first query that sees the NaN
+    for i, ch in ((0, 3), (1, 64), (n_q - 1, 127)):
+        t = lens[0] - n_q + i
+        kc.v[table[0, t // page], 0, t % page, ch] = 0xff if i else 0x7f
+        first[ch] = i
+    t = lens[0] - n_q + n_q // 2
+    kc.k[table[0, t // page], 1, t % page, 5] = 0x7f
+    out, _ = _attend(q, kc, table, lens, G)
+    for i in range(n_q):
+        nan = [ch for ch, f in first.items() if f <= i]
+        rest = [ch for ch in range(D) if ch not in nan]
+        assert bool(out[0, :G, i][:, nan].isnan().all())
+        assert torch.equal(out[0, :G, i][:, rest], clean[0, :G, i][:, rest])
+        if i < n_q // 2:
+            assert torch.equal(out[0, G:, i], clean[0, G:, i])
+        else:
+            assert bool(out[0, G:, i].isnan().all())
+
+
 def test_attn_flags_bad_lengths_and_pages():
     kc, table = _context([112, 100], 2, 16, SPARK_KV8_E4M3, 4)
     q = _values(_gen(5), (2, 8, 2, D))
