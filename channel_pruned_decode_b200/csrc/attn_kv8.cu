@@ -31,25 +31,38 @@ namespace spark {
 
 bool make_kv8_map(CUtensorMap *tm, const void *codes, long rows, int box_rows);
 
-constexpr int kAtWarps = 8;                // warps per CTA
-constexpr int kAtThreads = kAtWarps * 32;
+// Consumer warps of a CTA, for a kernel whose warps work on kNT groups of 8
+// query rows; a fourth or third warpgroup holds the producer (one warp works).
+// Registers per thread are dealt out from what the launch has (128 or 168):
+// 384 * 152 + 128 * 56 = 512 * 128, and 256 * 224 + 128 * 56 = 384 * 168.
+constexpr int kMaxTeams = 12;
+template <int kNT> struct AtGeom {
+    static constexpr int kWarps = kNT == 2 ? 8 : 12;
+    static constexpr int kThreads = (kWarps + 4) * 32;
+    static constexpr int kRegsConsumer = kNT == 2 ? 224 : 152;
+    static constexpr int kRegsProducer = 56;
+};
 constexpr int kStep = 32;                  // tokens per step
 constexpr int kStageBytes = 2 * kStep * kD;
-constexpr int kRingBytes = 24 * kStageBytes;  // all stages of a CTA: 192 KB
-constexpr int kMaxStages = 24;
+constexpr int kMaxStages = 24;             // stages of a CTA: 192 KB
+constexpr int kRingBytes = kMaxStages * kStageBytes;
 constexpr int kMinSteps = 2;               // a team takes at least this many steps
+constexpr int kPScale = 6;                 // probabilities enter the second product times 2^6
+constexpr float kSlack = 8.f;              // log2 of how far a probability may pass its reference
 
-// What a stage's consumer needs to know beside the codes.
-struct StageMeta {
-    float ks[2], vs[2];
-    int nv[2];        // seen tokens of each half (0 .. 16)
-    int pad[2];
+// What a stage's consumers need to know beside the codes.
+struct __align__(16) StageMeta {
+    float ks[2], vs[2];      // scales of the two halves (16 tokens each)
+    int nv[2];               // seen tokens of each half (0 .. 16)
+    int b, h;
+    int s, n_steps, len;     // step of the row, steps and tokens of the row
+    int pad;
 };
 
 // workspace: header, the line's layout (int64: steps per team, then steps
 // before each row), then partials: acc [slot][rows][128], ml [slot][rows][2]
 static size_t attn_layout_bytes(int B) { return (((size_t)B + 1) * 8 + 255) / 256 * 256; }
-static long attn_slots(int B, int Hkv, int num_sms) { return (long)num_sms * kAtWarps + (long)B * Hkv; }
+static long attn_slots(int B, int Hkv, int num_sms) { return (long)num_sms * kMaxTeams + (long)B * Hkv; }
 
 size_t attn_kv8_workspace(int B, int Hkv, int rows, int num_sms) {
     return kWsHeader + attn_layout_bytes(B) + (size_t)attn_slots(B, Hkv, num_sms) * rows * (kD + 2) * sizeof(float);
@@ -158,51 +171,33 @@ __device__ __forceinline__ void next_pair(const AttnArgs &a, Place &p) {
     while (p.n_steps == 0);
 }
 
-// Up to 16 steps of one pair: lane i holds the page and scales of half i (16 tokens).
-struct Batch {
+// One step as the producer sees it: the pages of its halves, then their scales.
+struct StepLoad {
     Place p;
-    int n;      // steps
-    int pg;
-    float ks, vs;
+    int pg[2];
+    float ks[2], vs[2];
 };
 
-__device__ __forceinline__ Batch load_batch(const AttnArgs &a, const Place &p, int n, bool *bad) {
-    const int lane = threadIdx.x & 31;
-    Batch t;
-    t.p = p;
-    t.n = n;
-    t.pg = -1;
-    t.ks = t.vs = 0.f;
-    const int tok = p.s * kStep + lane * 16;
-    if (tok < p.len && lane < 2 * n) {
-        const int pg = __ldg(a.table + (size_t)p.b * a.table_cap + tok / a.kc.page);
-        if (pg >= 0 && pg < a.kc.n_pages) {
-            t.pg = pg;
-            t.ks = __ldg(a.kc.k_scale + (size_t)pg * a.kc.Hkv + p.h);
-            t.vs = __ldg(a.kc.v_scale + (size_t)pg * a.kc.Hkv + p.h);
-        } else {
-            *bad = true;
-        }
-    }
-    return t;
-}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) { return mbar_try_wait(bar, parity); }
 
 // kNT: 8-row groups a warp works on; 0: up to 4 rows, whose second copy in
 // the group's other 4 places carries P's low halves through the same product.
 template <typename E, int kType, int kNT>
-__global__ void __launch_bounds__(kAtThreads, 1)
+__global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const E *__restrict__ q, const AttnArgs a) {
+    constexpr int kAtWarps = AtGeom<kNT>::kWarps, kAtThreads = AtGeom<kNT>::kThreads;
     constexpr int kN = kNT ? kNT : 1;              // 8-row groups
     constexpr int kRows = kNT ? 8 * kNT : 4;       // query rows of a warp
     constexpr int kQ = sizeof(E) == 4 ? 2 : 1;     // fp16 halves of a query
     extern __shared__ unsigned char sm_raw[];
     __shared__ long long before[kAtThreads + 1];   // steps (of one kv head) before each thread's rows
+    __shared__ long long wsum[kAtThreads / 32];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ StageMeta meta[kMaxStages];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int tw = a.team_warps, n_teams = kAtWarps / tw, team = warp / tw, wt = warp % tw;
-    const int Hkv = a.kc.Hkv, page = a.kc.page;
+    const int Hkv = a.kc.Hkv, ns = a.n_stages;
     const uint32_t ring = (smem_u32(sm_raw) + 1023u) & ~1023u;
 
     // ---- the line: steps before each thread's rows, and in all
@@ -225,7 +220,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const long long y = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += y;
         }
-        __shared__ long long wsum[kAtWarps];
         if (lane == 31) wsum[warp] = v;
         if (tid < kMaxStages) {
             mbar_init(smem_u32(&full[tid]), 1);
@@ -253,118 +247,165 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const long long all_teams = (long long)gridDim.x * n_teams;
     const long long share = max((total + all_teams - 1) / all_teams, (long long)kMinSteps);
     if (blockIdx.x == 0 && tid == 0) a.layout[0] = share;
-    if (team >= n_teams) return;  // warps that make no whole team
-    const long long tm = (long long)team * gridDim.x + blockIdx.x;
-    const long long from = tm * share;
-    if (from >= total) return;
-    int left = (int)min(share, total - from);  // steps of this team
 
-    Place p;
-    {
-        int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before `from`
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (before[mid] * Hkv <= from) lo = mid;
-            else hi = mid;
-        }
-        long long pos = from - before[lo] * Hkv;
-        int b = lo * per;
-        for (;;) {
-            set_row(a, p, b);
-            if (pos < (long long)p.n_steps * Hkv) break;
-            pos -= (long long)p.n_steps * Hkv;
-            ++b;
-        }
-        p.h = (int)(pos / p.n_steps);
-        p.s = (int)(pos % p.n_steps);
-    }
-
-    const int ns = a.n_stages, st0 = team * ns;
-    const uint32_t base = ring + (uint32_t)st0 * kStageBytes;
-    bool bad = false, failed = false;
-
-    // ---- producer (the team's first warp): keeps the ring full
-    Batch cur, nxt;
-    int to_load = left, to_issue = left, in_cur = 0;  // steps not yet in a batch / not yet issued; place in cur
-    Place pl = p;
-    auto fetch = [&]() {
-        Batch t = cur;
-        t.n = 0;
-        if (to_load > 0) {
+    if (warp >= kAtWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AtGeom<kNT>::kRegsProducer));
+        if (warp > kAtWarps) return;
+        // ---- producer: lane t keeps team t's part of the ring full
+        const long long from = ((long long)blockIdx.x * n_teams + lane) * share;
+        int left = lane < n_teams && from < total ? (int)min(share, total - from) : 0;
+        bool bad = false;
+        const int page = a.kc.page, shift = 31 - __clz(page);
+        StepLoad d0, d1;
+        Place pl = {0, 0, 0, 0, 0};
+        int to_load = left;
+        // pages of the next step that has none yet
+        auto load_pages = [&](StepLoad &d) {
+            d.pg[0] = d.pg[1] = -1;
+            if (to_load == 0) return;
             if (pl.s == pl.n_steps) next_pair(a, pl);
-            const int n = min(min(16, pl.n_steps - pl.s), to_load);
-            t = load_batch(a, pl, n, &bad);
-            pl.s += n;
-            to_load -= n;
-        }
-        return t;
-    };
-    auto issue = [&](int st) {  // the next step into stage st
-        if (in_cur == cur.n) {
-            cur = nxt;
-            in_cur = 0;
-            nxt = fetch();
-        }
-        const int pg0 = __shfl_sync(0xffffffffu, cur.pg, 2 * in_cur), pg1 = __shfl_sync(0xffffffffu, cur.pg, 2 * in_cur + 1);
-        const float k0 = __shfl_sync(0xffffffffu, cur.ks, 2 * in_cur), k1 = __shfl_sync(0xffffffffu, cur.ks, 2 * in_cur + 1);
-        const float v0 = __shfl_sync(0xffffffffu, cur.vs, 2 * in_cur), v1 = __shfl_sync(0xffffffffu, cur.vs, 2 * in_cur + 1);
-        if (lane == 0) {
-            const int tok = (cur.p.s + in_cur) * kStep, len = cur.p.len;
-            StageMeta &m = meta[st0 + st];
-            m.ks[0] = k0;
-            m.ks[1] = k1;
-            m.vs[0] = v0;
-            m.vs[1] = v1;
-            m.nv[0] = pg0 >= 0 ? min(16, len - tok) : 0;
-            m.nv[1] = pg1 >= 0 ? min(16, len - tok - 16) : 0;  // pg1 < 0 past the row's end
-            const uint32_t bar = smem_u32(&full[st0 + st]), dst = base + (uint32_t)st * kStageBytes;
-            if (page >= kStep) {
-                mbar_expect_tx(bar, pg0 >= 0 ? 2 * kStep * kD : 0);
-                if (pg0 >= 0) {
-                    const int row = (pg0 * Hkv + cur.p.h) * page + (tok & (page - 1));
-                    tma_rows(dst, &map_k, row, bar);
-                    tma_rows(dst + kStep * kD, &map_v, row, bar);
+            d.p = pl;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tok = pl.s * kStep + i * 16;
+                if (tok < pl.len) d.pg[i] = __ldg(a.table + (size_t)pl.b * a.table_cap + (tok >> shift));
+            }
+            ++pl.s;
+            --to_load;
+        };
+        auto load_scales = [&](StepLoad &d) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                d.ks[i] = d.vs[i] = 0.f;
+                const bool ok = (unsigned)d.pg[i] < (unsigned)a.kc.n_pages;
+                if (ok) {
+                    d.ks[i] = __ldg(a.kc.k_scale + (size_t)d.pg[i] * Hkv + d.p.h);
+                    d.vs[i] = __ldg(a.kc.v_scale + (size_t)d.pg[i] * Hkv + d.p.h);
                 }
+            }
+        };
+        if (left > 0) {
+            int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before `from`
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (before[mid] * Hkv <= from) lo = mid;
+                else hi = mid;
+            }
+            long long pos = from - before[lo] * Hkv;
+            for (int b = lo * per;; ++b) {
+                set_row(a, pl, b);
+                if (pos < (long long)pl.n_steps * Hkv) break;
+                pos -= (long long)pl.n_steps * Hkv;
+            }
+            pl.h = (int)(pos / pl.n_steps);
+            pl.s = (int)(pos % pl.n_steps);
+            load_pages(d0);
+            load_scales(d0);
+            load_pages(d1);
+        }
+        const int st0 = lane * ns;
+        int st = 0;
+        uint32_t parity = 1;  // a fresh barrier passes
+        uint64_t since = global_ns();
+        bool failed = false;
+        while (__any_sync(0xffffffffu, left > 0)) {
+            const bool ready = left > 0 && mbar_test(smem_u32(&empty[st0 + st]), parity);
+            if (ready) {
+                const int tok = d0.p.s * kStep, len = d0.p.len;
+                bool ok[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ok[i] = (unsigned)d0.pg[i] < (unsigned)a.kc.n_pages;
+                    bad |= !ok[i] && tok + i * 16 < len;
+                }
+                StageMeta &m = meta[st0 + st];
+                m.ks[0] = d0.ks[0];
+                m.ks[1] = d0.ks[1];
+                m.vs[0] = d0.vs[0];
+                m.vs[1] = d0.vs[1];
+                m.nv[0] = ok[0] ? min(16, len - tok) : 0;
+                m.nv[1] = ok[1] ? min(16, len - tok - 16) : 0;
+                m.b = d0.p.b;
+                m.h = d0.p.h;
+                m.s = d0.p.s;
+                m.n_steps = d0.p.n_steps;
+                m.len = len;
+                const uint32_t bar = smem_u32(&full[st0 + st]), dst = ring + (uint32_t)(st0 + st) * kStageBytes;
+                if (page >= kStep) {
+                    mbar_expect_tx(bar, ok[0] ? 2 * kStep * kD : 0);
+                    if (ok[0]) {
+                        const int row = (d0.pg[0] * Hkv + d0.p.h) * page + (tok & (page - 1));
+                        tma_rows(dst, &map_k, row, bar);
+                        tma_rows(dst + kStep * kD, &map_v, row, bar);
+                    }
+                } else {
+                    mbar_expect_tx(bar, (ok[0] + ok[1]) * 2 * 16 * kD);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (ok[i]) {
+                            const int row = (d0.pg[i] * Hkv + d0.p.h) * 16;
+                            tma_rows(dst + i * 16 * kD, &map_k, row, bar);
+                            tma_rows(dst + (kStep + i * 16) * kD, &map_v, row, bar);
+                        }
+                }
+                --left;
+                if (++st == ns) {
+                    st = 0;
+                    parity ^= 1;
+                }
+                d0 = d1;
+                load_scales(d0);
+                load_pages(d1);
+            }
+            if (__any_sync(0xffffffffu, ready)) {
+                since = global_ns();
             } else {
-                mbar_expect_tx(bar, ((pg0 >= 0) + (pg1 >= 0)) * 2 * 16 * kD);
-                if (pg0 >= 0) {
-                    const int row = (pg0 * Hkv + cur.p.h) * 16;
-                    tma_rows(dst, &map_k, row, bar);
-                    tma_rows(dst + kStep * kD, &map_v, row, bar);
-                }
-                if (pg1 >= 0) {
-                    const int row = (pg1 * Hkv + cur.p.h) * 16;
-                    tma_rows(dst + 16 * kD, &map_k, row, bar);
-                    tma_rows(dst + (kStep + 16) * kD, &map_v, row, bar);
+                __nanosleep(40);
+                if (global_ns() - since > 1000000000ull) {
+                    failed = true;
+                    break;
                 }
             }
         }
-        ++in_cur;
-        --to_issue;
-    };
-    if (wt == 0) {
-        cur.p = p;
-        cur.n = 0;
-        cur.pg = -1;
-        cur.ks = cur.vs = 0.f;
-        cur = fetch();
-        nxt = fetch();
-        for (int st = 0; st < ns && to_issue > 0; ++st) issue(st);
+        if (bad) atomicOr(a.ws, kDevBadArg);
+        if (failed) {
+            // some consumer gave up; let the copies in flight land before the CTA's memory goes away
+            if (lane == 0) atomicOr(a.ws, kDevTimeout);
+            if (lane < n_teams)
+                for (int i = 0; i < ns; ++i) {
+                    const int u = (st + i) % ns;  // its last use had this parity (of a stage never used, 1: passes)
+                    mbar_wait_bounded(smem_u32(&full[st0 + u]), st + i < ns ? parity : parity ^ 1u);
+                }
+        }
+        return;
     }
 
-    // ---- consumer
+    // ---- consumers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AtGeom<kNT>::kRegsConsumer));
+    if (team >= n_teams) return;  // warps that make no whole team
+    const long long tm = (long long)blockIdx.x * n_teams + team;
+    const long long from = tm * share;
+    if (from >= total) return;
+    const int steps = (int)min(share, total - from);
+    const int st0 = team * ns;
+    const uint32_t base = ring + (uint32_t)st0 * kStageBytes;
+
     uint32_t qh[kQ][kN][16];      // B fragments of the queries
     float qf[kN][2];              // score factor of rows 2c, 2c + 1
     int lim[kN][2];               // the last token they see
-    float o[kN][8][4], m[kN][2], l[kN][2], E_top;
-    int nn = 0, first_full = 0;
-    bool starts_pair = p.s == 0;  // this team has the pair's first step
-    auto begin_pair = [&]() {
-        nn = a.n_new ? min(max(__ldg(a.n_new + p.b), 0), a.n_q) : a.n_q;
-        first_full = p.len - nn + 1;  // tokens below this are seen by every query
-        starts_pair = p.s == 0;
+    float o[kN][8][4], m[kN][2], l[kN][2];
+    float E_top = 1.f, E_inv = 1.f;
+    int b = -1, h = 0, nn = 0, first_full = 0;
+    bool starts_pair = false, ends_pair = false;
+    auto begin_pair = [&](const StageMeta &mt) {
+        b = mt.b;
+        h = mt.h;
+        nn = a.n_new ? min(max(__ldg(a.n_new + b), 0), a.n_q) : a.n_q;
+        first_full = mt.len - nn + 1;  // tokens below this are seen by every query
+        starts_pair = mt.s == 0;
         E_top = exp2_int(-100);
-        const E *qb = q + ((size_t)p.b * Hkv + p.h) * a.rows * kD;
+        E_inv = exp2_int(100 + kPScale);
+        const E *qb = q + ((size_t)b * Hkv + h) * a.rows * kD;
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
             const int r = wt * kRows + (kNT ? t * 8 + g : (g & 3));
@@ -404,7 +445,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 qf[t][j] = __shfl_sync(0xffffffffu, mine, (2 * c + j) * 4);
                 const int col = kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3;
                 const int row = wt * kRows + col, i = row % a.n_q;
-                lim[t][j] = row < a.rows && i < nn ? p.len - nn + i : -1;
+                lim[t][j] = row < a.rows && i < nn ? mt.len - nn + i : -1;
                 m[t][j] = -INFINITY;
                 l[t][j] = 0.f;
             }
@@ -412,8 +453,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
         }
     };
-    auto end_pair = [&](bool ends_pair) {
-        const long bh = (long)p.b * Hkv + p.h;
+    auto end_pair = [&]() {
+        const long bh = (long)b * Hkv + h;
         const bool whole = starts_pair && ends_pair;
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
@@ -437,7 +478,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int row = wt * kRows + col;
                 if ((kNT == 0 && c >= 2) || row >= a.rows || row % a.n_q >= nn) continue;
                 float *dst;
-                float f = E_top * exp2_int(-14);
+                float f = E_top * exp2_int(-kPScale);
                 if (whole) {
                     dst = a.out + (bh * a.rows + row) * kD;
                     f = l[t][j] == 0.f ? 0.f : f / l[t][j];
@@ -455,23 +496,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
     };
 
-    begin_pair();
     int st = 0;
     uint32_t parity = 0;
-    for (int it = 0; it < left; ++it) {
-        if (p.s == p.n_steps) {
-            end_pair(true);
-            next_pair(a, p);
-            begin_pair();
-        }
+    for (int it = 0; it < steps; ++it) {
         if (!mbar_wait_bounded(smem_u32(&full[st0 + st]), parity)) {
-            failed = true;
-            break;
+            if (lane == 0) atomicOr(a.ws, kDevTimeout);
+            return;
         }
         const StageMeta mt = meta[st0 + st];
+        if (mt.b != b || mt.h != h) {
+            if (b >= 0) end_pair();
+            begin_pair(mt);
+        }
+        ends_pair = mt.s + 1 == mt.n_steps;
         const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
-        const int t0 = p.s * kStep;
-        const bool edge = mt.nv[0] < 16 || mt.nv[1] < 16 || t0 + kStep > first_full;
+        const int t0 = mt.s * kStep;
 
         // scores
         float s[kN][2][4];
@@ -499,111 +538,120 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
             }
         }
-        // running maximum, in units of log2
-        float cf[2];
-        {
-            const float vm = fmaxf(mt.vs[0], mt.vs[1]);
+        // places without a token and tokens behind a query's own
+        const bool edge = mt.nv[0] < 16 || mt.nv[1] < 16 || t0 + kStep > first_full;
+        bool hide = false;
+        if (edge) {
+#pragma unroll
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int in = g + 8 * (i >> 1);
+                        if (in >= mt.nv[hf] || t0 + hf * 16 + in > lim[t][i & 1]) s[t][hf][i] = -INFINITY;
+                    }
+            // Places without a token may hold anything, NaN codes too: their
+            // values become zeros before the second product meets them.
+            if (mt.nv[0] < 16 || mt.nv[1] < 16) {
+                for (int i = lane; i < kStep * 8; i += 32) {
+                    const int row = i >> 3;
+                    if ((row & 15) >= (row < 16 ? mt.nv[0] : mt.nv[1]))
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (uint32_t)i * 16), "r"(0u)
+                                     : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            // A token that some of the queries do not see takes part in the second
+            // product with p = 0 for them: where its value is NaN, the queries that
+            // see it get their NaN here and the product a zero.
+            if (kType == SPARK_KV8_E4M3 && a.n_q > 1) {
+#pragma unroll 1
+                for (int i = max(first_full - t0, 0); i < kStep; ++i) {
+                    if ((i & 15) >= (i < 16 ? mt.nv[0] : mt.nv[1])) continue;
+                    const uint4 w = lds128(vb + (uint32_t)i * kD + ((uint32_t)(g ^ (i & 7)) << 4));
+                    const uint32_t ww[4] = {nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w)};
+                    if (!__any_sync(0xffffffffu, (ww[0] | ww[1] | ww[2] | ww[3]) != 0)) continue;
+                    hide = true;
+#pragma unroll
+                    for (int t = 0; t < kN; ++t)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if (((ww[j / 4] >> (8 * (j % 4))) & 0xffu) && t0 + i <= lim[t][y])
+                                    o[t][j / 2][(j & 1) * 2 + y] = __int_as_float(0x7fffffff);
+                }
+            }
+        }
+        // The reference m of a row's probabilities (in units of log2) is its
+        // largest score so far, but follows it only when that is more than
+        // kSlack above: the sums take any reference, and most steps then
+        // need no maximum across lanes and no rescaling.
+        float f[kN][2][2];
+        bool move = false;
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // above 0, so that an unseen place stays at -inf whatever its page's scale
+                f[t][0][j] = fmaxf(qf[t][j] * mt.ks[0], exp2_int(-126));
+                f[t][1][j] = fmaxf(qf[t][j] * mt.ks[1], exp2_int(-126));
+                const float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
+                                       fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
+                move |= mx > m[t][j] + kSlack;
+            }
+        const float vm = fmaxf(mt.vs[0], mt.vs[1]);
+        if (__any_sync(0xffffffffu, move || vm > E_top)) {
             float grow = 1.f;
             if (vm > E_top) {
                 const float top = __uint_as_float((__float_as_uint(vm) & 0x7f800000u) + 0x800000u);
                 grow = E_top / top;
                 E_top = top;
+                E_inv = exp2_int(kPScale) / top;
             }
-            const float inv = exp2_int(14) / E_top;
-            cf[0] = mt.vs[0] * inv;
-            cf[1] = mt.vs[1] * inv;
-            bool moved = grow != 1.f;
-            float al[kN][2];
 #pragma unroll
-            for (int t = 0; t < kN; ++t)
+            for (int t = 0; t < kN; ++t) {
+                float al[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float f = qf[t][j] * mt.ks[hf];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float &x = s[t][hf][2 * r + j];
-                            x *= f;
-                            if (edge) {
-                                const int in = g + 8 * r;
-                                if (in >= mt.nv[hf] || t0 + hf * 16 + in > lim[t][j]) x = -INFINITY;
-                            }
-                            mx = fmaxf(mx, x);
-                        }
-                    }
+                    float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
+                                     fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                     const float mn = fmaxf(m[t][j], mx);
-                    al[t][j] = mn > m[t][j] ? exp2_approx(m[t][j] - mn) : 1.f;  // 0 from -inf
-                    moved |= mn > m[t][j];
+                    al[j] = mn > m[t][j] ? exp2_approx(m[t][j] - mn) : 1.f;  // 0 from -inf
                     m[t][j] = mn;
+                    l[t][j] *= al[j];
+                    al[j] *= grow;
                 }
-            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int t = 0; t < kN; ++t) {
-                    l[t][0] *= al[t][0];
-                    l[t][1] *= al[t][1];
-                    const float f0 = al[t][0] * grow, f1 = al[t][1] * grow;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[t][j][0] *= f0;
-                        o[t][j][1] *= f1;
-                        o[t][j][2] *= f0;
-                        o[t][j][3] *= f1;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    o[t][j][0] *= al[0];
+                    o[t][j][1] *= al[1];
+                    o[t][j][2] *= al[0];
+                    o[t][j][3] *= al[1];
                 }
-            }
-        }
-        // places without a token may hold anything, NaN codes too: they
-        // become zeros before the second product meets them
-        if (mt.nv[0] < 16 || mt.nv[1] < 16) {
-            for (int i = lane; i < kStep * 8; i += 32) {
-                const int row = i >> 3;
-                if ((row & 15) >= mt.nv[row >> 4])
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (uint32_t)i * 16), "r"(0u)
-                                 : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        // A token that some of the queries do not see takes part in the second
-        // product with p = 0 for them: where its value is NaN, the queries that
-        // see it get their NaN here and the product a zero.
-        bool hide = false;
-        if (kType == SPARK_KV8_E4M3 && a.n_q > 1 && t0 + kStep > first_full) {
-            for (int i = max(first_full - t0, 0); i < kStep; ++i) {
-                if ((i & 15) >= mt.nv[i >> 4]) continue;
-                const uint4 w = lds128(vb + (uint32_t)i * kD + ((uint32_t)(g ^ (i & 7)) << 4));
-                const uint32_t ww[4] = {nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w)};
-                if (!__any_sync(0xffffffffu, (ww[0] | ww[1] | ww[2] | ww[3]) != 0)) continue;
-                hide = true;
-#pragma unroll
-                for (int t = 0; t < kN; ++t)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            if (((ww[j / 4] >> (8 * (j % 4))) & 0xffu) && t0 + i <= lim[t][y])
-                                o[t][j / 2][(j & 1) * 2 + y] = __int_as_float(0x7fffffff);
             }
         }
         // probabilities, their sums, and the second product
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
+            const float cf = mt.vs[hf] * E_inv;
             uint32_t ph[kN][2], pl_[kN][2];
 #pragma unroll
             for (int t = 0; t < kN; ++t) {
                 const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float p0 = exp2_approx(s[t][hf][2 * r] - m0), p1 = exp2_approx(s[t][hf][2 * r + 1] - m1);
+                    float p0 = exp2_approx(s[t][hf][2 * r] * f[t][hf][0] - m0);
+                    float p1 = exp2_approx(s[t][hf][2 * r + 1] * f[t][hf][1] - m1);
                     l[t][0] += p0;
                     l[t][1] += p1;
-                    p0 *= cf[hf];
-                    p1 *= cf[hf];
+                    p0 *= cf;
+                    p1 *= cf;
                     const __half2 hi = __floats2half2_rn(p0, p1);
                     const float2 back = __half22float2(hi);
                     const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);
@@ -626,14 +674,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     w[i] = make_uint4(w[i].x & ~nan_codes(w[i].x), w[i].y & ~nan_codes(w[i].y),
                                       w[i].z & ~nan_codes(w[i].z), w[i].w & ~nan_codes(w[i].w));
             }
+            const uint32_t ww[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
+                                       {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t x0 = (&w[0].x)[j], x1 = (&w[1].x)[j], x2 = (&w[2].x)[j], x3 = (&w[3].x)[j];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     uint32_t a0, a1, a2, a3;
-                    expand4<kType>(__byte_perm(x0, x1, y ? 0x7362 : 0x5140), a0, a1);
-                    expand4<kType>(__byte_perm(x2, x3, y ? 0x7362 : 0x5140), a2, a3);
+                    expand4<kType>(__byte_perm(ww[0][j], ww[1][j], y ? 0x7362 : 0x5140), a0, a1);
+                    expand4<kType>(__byte_perm(ww[2][j], ww[3][j], y ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
                     for (int t = 0; t < kN; ++t) {
                         mma16816(o[t][2 * j + y], a0, a1, a2, a3, ph[t][0], ph[t][1]);
@@ -644,30 +693,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         // the stage is free once every warp of the team has read it
         __syncwarp();
-        if (tw > 1 && lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
-        if (wt == 0 && to_issue > 0) {
-            if (tw > 1 && !mbar_wait_bounded(smem_u32(&empty[st0 + st]), parity)) {
-                failed = true;
-                break;
-            }
-            issue(st);
-        }
-        ++p.s;
+        if (lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
         if (++st == ns) {
             st = 0;
             parity ^= 1;
         }
     }
-    if (failed) {
-        if (lane == 0) atomicOr(a.ws, kDevTimeout);
-        // let the copies in flight land before the CTA's memory goes away
-        if (wt == 0)
-            for (int i = 0; i < ns; ++i)
-                mbar_wait_bounded(smem_u32(&full[st0 + (st + i) % ns]), parity ^ (uint32_t)(st + i >= ns));
-        return;
-    }
-    end_pair(p.s == p.n_steps);
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.ws, kDevBadArg);
+    end_pair();
 }
 
 // Merge of the partials of one query row: CTA = row, warps take partials in
@@ -731,7 +763,7 @@ static cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, cons
     auto kernel = attn_kv8_kernel<E, kType, kNT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)num_sms, kAtThreads, smem, st>>>(mk, mv, static_cast<const E *>(q), a);
+    kernel<<<(unsigned)num_sms, AtGeom<kNT>::kThreads, smem, st>>>(mk, mv, static_cast<const E *>(q), a);
     return cudaGetLastError();
 }
 
@@ -741,7 +773,7 @@ static cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, con
     // rows a warp works on; two groups of 8 only for bf16 queries, whose fragments take half the registers
     const int per = a.rows <= 4 ? 4 : (a.rows <= 8 || sizeof(E) == 4) ? 8 : 16;
     a.team_warps = (a.rows + per - 1) / per;
-    const int teams = kAtWarps / a.team_warps;
+    const int teams = (per == 16 ? AtGeom<2>::kWarps : AtGeom<1>::kWarps) / a.team_warps;
     a.n_stages = min(kMaxStages / teams, 8);
     if (per == 4) return launch_one<E, kType, 0>(mk, mv, q, a, num_sms, st);
     if (per == 8) return launch_one<E, kType, 1>(mk, mv, q, a, num_sms, st);
