@@ -496,7 +496,9 @@ int spark_decode_attn_kv8(const void *q, int dtype, const spark_kv8cache *kc, co
     if (rc != SPARK_OK) return rc;
     if (B < 0 || table_cap < 0 || G < 1 || n_q < 1 || elem_size(dtype) == 0) return SPARK_ERR_ARG;
     if ((long)G * n_q > kKv8MaxRows) return SPARK_ERR_UNSUPPORTED;
-    if ((double)table_cap * kc->page > 2147483647.0 || (double)B * kc->Hkv * kKv8MaxRows > 2147483647.0)
+    // 32-bit counts of a row's tokens, of query rows, and of 32-token steps of all heads
+    if ((double)table_cap * kc->page > 2147483647.0 || (double)B * kc->Hkv * kKv8MaxRows > 2147483647.0 ||
+        (double)B * kc->Hkv * ((table_cap * (long)kc->page + 31) / 32) > 2147483647.0)
         return SPARK_ERR_UNSUPPORTED;
     if ((long)B * kc->Hkv == 0) return SPARK_OK;
     if (!q || !aligned16(q) || !out || !aligned16(out) || !lens || !aligned4(lens) || !aligned4(n_new))

@@ -31,22 +31,18 @@ namespace spark {
 
 bool make_kv8_map(CUtensorMap *tm, const void *codes, long rows, int box_rows);
 
-// Consumer warps of a CTA, for a kernel whose warps work on kNT groups of 8
-// query rows; a fourth or third warpgroup holds the producer (one warp works).
-// Registers per thread are dealt out from what the launch has (128 or 168):
-// 384 * 152 + 128 * 56 = 512 * 128, and 256 * 224 + 128 * 56 = 384 * 168.
+// Warps of a CTA, for a kernel whose warps work on kNT groups of 8 query rows
+// (168 or 255 registers a thread).
 constexpr int kMaxTeams = 12;
 template <int kNT> struct AtGeom {
     static constexpr int kWarps = kNT == 2 ? 8 : 12;
-    static constexpr int kThreads = (kWarps + 4) * 32;
-    static constexpr int kRegsConsumer = kNT == 2 ? 224 : 152;
-    static constexpr int kRegsProducer = 56;
+    static constexpr int kThreads = kWarps * 32;
 };
 constexpr int kStep = 32;                  // tokens per step
 constexpr int kStageBytes = 2 * kStep * kD;
 constexpr int kMaxStages = 24;             // stages of a CTA: 192 KB
 constexpr int kRingBytes = kMaxStages * kStageBytes;
-constexpr int kMinSteps = 2;               // a team takes at least this many steps
+constexpr int kMinCtaSteps = 4;            // a CTA takes at least this many steps
 constexpr int kPScale = 6;                 // probabilities enter the second product times 2^6
 constexpr float kSlack = 8.f;              // log2 of how far a probability may pass its reference
 
@@ -59,13 +55,17 @@ struct __align__(16) StageMeta {
     int pad;
 };
 
-// workspace: header, the line's layout (int64: steps per team, then steps
-// before each row), then partials: acc [slot][rows][128], ml [slot][rows][2]
-static size_t attn_layout_bytes(int B) { return (((size_t)B + 1) * 8 + 255) / 256 * 256; }
-static long attn_slots(int B, int Hkv, int num_sms) { return (long)num_sms * kMaxTeams + (long)B * Hkv; }
+// Workspace: header, one counter per CTA (zero between calls), then the
+// partials of teams and of CTAs: acc [slot][rows][128] fp32, and (m, l)
+// [slot][rows][2].  Along the line the team and the pair only grow, so team +
+// pair numbers a team's partial of a pair uniquely, and CTA + pair a CTA's.
+static size_t attn_counter_bytes(int num_sms) { return ((size_t)num_sms * 4 + 255) / 256 * 256; }
+static long attn_team_slots(long pairs, int num_sms) { return (long)num_sms * kMaxTeams + pairs; }
 
 size_t attn_kv8_workspace(int B, int Hkv, int rows, int num_sms) {
-    return kWsHeader + attn_layout_bytes(B) + (size_t)attn_slots(B, Hkv, num_sms) * rows * (kD + 2) * sizeof(float);
+    const long pairs = (long)B * Hkv;
+    const size_t slots = (size_t)(attn_team_slots(pairs, num_sms) + num_sms + pairs);
+    return kWsHeader + attn_counter_bytes(num_sms) + slots * rows * (kD + 2) * sizeof(float);
 }
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *tm, int row, uint32_t bar) {
@@ -74,6 +74,38 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *tm, in
             dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(row), "r"(bar)
         : "memory");
+}
+
+// A value that is the same in all lanes, in a form from which the compiler
+// knows that.  One branch in a loop whose condition may differ between lanes
+// for all the compiler knows (a loaded number, say), with a shuffle or a vote
+// behind it, and every shuffle, vote and transpose of the loop becomes a
+// call-like sequence of some 200 cycles.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x) != 0; }
+
+// The same value, of which the compiler knows nothing.  Conditions on launch
+// constants inside the main loop go through this: the compiler would make a
+// copy of the whole loop for each outcome of each of them (110 KB of code
+// instead of 19), and what a CTA runs once costs what its fetch costs.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
+// Bounded wait of a whole warp (about 1 s); the answer is the same in all
+// lanes.  Written without unrolling: it is code that every CTA fetches.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t since = global_ns();
+#pragma unroll 1
+        for (uint32_t it = 0; !ok && it < (1u << 26); ++it) {
+            ok = mbar_try_wait(bar, parity);
+            if ((it & 63u) == 63u && global_ns() - since > 1000000000ull) break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -147,9 +179,9 @@ struct AttnArgs {
     const int32_t *table, *lens, *n_new;
     int table_cap, B, rows, n_q, team_warps, n_stages;
     float *out;
-    uint32_t *ws;
-    long long *layout;
-    float *acc, *ml;
+    uint32_t *ws, *counter;
+    float *acc, *ml;        // team partials
+    float *acc_c, *ml_c;    // CTA partials
 };
 
 __device__ __forceinline__ int clamped_len(const AttnArgs &a, int b) {
@@ -167,18 +199,91 @@ __device__ __forceinline__ void next_pair(const AttnArgs &a, Place &p) {
     p.s = 0;
     if (++p.h < a.kc.Hkv) return;
     p.h = 0;
-    do set_row(a, p, p.b + 1);
-    while (p.n_steps == 0);
+#pragma unroll 1
+    do {
+        set_row(a, p, p.b + 1);
+        p.len = uniform(p.len);
+        p.n_steps = uniform(p.n_steps);
+    } while (p.n_steps == 0);
 }
 
-// One step as the producer sees it: the pages of its halves, then their scales.
-struct StepLoad {
+// Up to 16 steps of one pair: lane i holds the page and scales of half i (16 tokens).
+struct Batch {
     Place p;
-    int pg[2];
-    float ks[2], vs[2];
+    int n;      // steps
+    int pg;     // -1: no page
+    float ks, vs;
 };
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) { return mbar_try_wait(bar, parity); }
+__device__ __forceinline__ void load_batch(const AttnArgs &a, const Place &p, int n, Batch &t, bool *bad) {
+    const int lane = threadIdx.x & 31;
+    t.p = p;
+    t.n = n;
+    t.pg = -1;
+    t.ks = t.vs = 0.f;
+    const int tok = p.s * kStep + lane * 16;
+    if (tok < p.len && lane < 2 * n) {
+        const int pg = __ldg(a.table + (size_t)p.b * a.table_cap + (tok >> (31 - __clz(a.kc.page))));
+        if ((unsigned)pg < (unsigned)a.kc.n_pages) {
+            t.pg = pg;
+            t.ks = __ldg(a.kc.k_scale + (size_t)pg * a.kc.Hkv + p.h);
+            t.vs = __ldg(a.kc.v_scale + (size_t)pg * a.kc.Hkv + p.h);
+        } else {
+            *bad = true;
+        }
+    }
+}
+
+// The first and the last pair of a team's stretch: number, and the first and
+// last team (counted over all CTAs) that have steps of it.
+struct Stretch {
+    int pair[2], t0[2], t1[2];
+};
+
+// What is left of `n` partials of one query row, read as (acc, ml) at stride
+// `rows`: lane i gets channels 4i .. 4i + 3 of acc = sum 2^(m_i - m) acc_i,
+// and m, l.  n <= 32 at a time; partials written by other CTAs are read past L1.
+struct Merged {
+    float m, l;
+    float4 acc;
+};
+
+__device__ __forceinline__ Merged merge_partials(const float *acc, const float *ml, int n, int rows) {
+    const int lane = threadIdx.x & 31;
+    Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int k = min(32, n - i0);
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (lane < k) x = __ldcg(reinterpret_cast<const float2 *>(ml + (size_t)(i0 + lane) * rows * 2));
+        float m = x.x;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = fmaxf(m, r.m);
+        // without any seen token every weight is 1 (of zeros)
+        const float e = m == -INFINITY ? 1.f : exp2_approx(x.x - m), old = m == -INFINITY ? 1.f : exp2_approx(r.m - m);
+        float l = x.y * e;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        r.l = r.l * old + l;
+        r.acc = make_float4(r.acc.x * old, r.acc.y * old, r.acc.z * old, r.acc.w * old);
+        r.m = m;
+        const float *at = acc + (size_t)i0 * rows * kD + lane * 4;
+#pragma unroll 4
+        for (int i = 0; i < k; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + (size_t)i * rows * kD));
+            const float w = __shfl_sync(0xffffffffu, e, i);
+            r.acc = make_float4(r.acc.x + v.x * w, r.acc.y + v.y * w, r.acc.z + v.z * w, r.acc.w + v.w * w);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ void write_row(float *out, const Merged &r) {
+    const float f = r.l == 0.f ? 0.f : 1.f / r.l;
+    reinterpret_cast<float4 *>(out)[threadIdx.x & 31] =
+        make_float4(r.acc.x * f, r.acc.y * f, r.acc.z * f, r.acc.w * f);
+}
 
 // kNT: 8-row groups a warp works on; 0: up to 4 rows, whose second copy in
 // the group's other 4 places carries P's low halves through the same product.
@@ -191,11 +296,14 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     constexpr int kRows = kNT ? 8 * kNT : 4;       // query rows of a warp
     constexpr int kQ = sizeof(E) == 4 ? 2 : 1;     // fp16 halves of a query
     extern __shared__ unsigned char sm_raw[];
-    __shared__ long long before[kAtThreads + 1];   // steps (of one kv head) before each thread's rows
-    __shared__ long long wsum[kAtThreads / 32];
+    __shared__ int before[kAtThreads + 1];   // steps (of one kv head) before each thread's rows
+    __shared__ int wsum[kAtThreads / 32];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ StageMeta meta[kMaxStages];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    __shared__ Stretch stretch[kMaxTeams];
+    __shared__ int last_c0[2], last_c1[2], last_pair[2];  // pairs that this CTA is the last to finish
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
     const int tw = a.team_warps, n_teams = kAtWarps / tw, team = warp / tw, wt = warp % tw;
     const int Hkv = a.kc.Hkv, ns = a.n_stages;
     const uint32_t ring = (smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -203,8 +311,9 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     // ---- the line: steps before each thread's rows, and in all
     const int per = (a.B + kAtThreads - 1) / kAtThreads;
     {
-        long long mine = 0;
+        int mine = 0;
         bool bad = false;
+#pragma unroll 1
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
             if (b < a.B) {
@@ -214,10 +323,10 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             }
         }
         if (bad && blockIdx.x == 0) atomicOr(a.ws, kDevBadArg);
-        long long v = mine;
+        int v = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, v, d);
+            const int y = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += y;
         }
         if (lane == 31) wsum[warp] = v;
@@ -227,169 +336,124 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncthreads();
-        long long pre = 0;
+        int pre = 0;
+#pragma unroll 1
         for (int w = 0; w < warp; ++w) pre += wsum[w];
         before[tid + 1] = pre + v;
         if (tid == 0) before[0] = 0;
         __syncthreads();
-        if (blockIdx.x == 0) {  // for the merge
-            long long x = before[tid];
-            for (int i = 0; i < per; ++i) {
-                const int b = tid * per + i;
-                if (b < a.B) {
-                    a.layout[1 + b] = x;
-                    x += (clamped_len(a, b) + kStep - 1) / kStep;
-                }
-            }
-        }
     }
-    const long long total = before[kAtThreads] * Hkv;
-    const long long all_teams = (long long)gridDim.x * n_teams;
-    const long long share = max((total + all_teams - 1) / all_teams, (long long)kMinSteps);
-    if (blockIdx.x == 0 && tid == 0) a.layout[0] = share;
-
-    if (warp >= kAtWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AtGeom<kNT>::kRegsProducer));
-        if (warp > kAtWarps) return;
-        // ---- producer: lane t keeps team t's part of the ring full
-        const long long from = ((long long)blockIdx.x * n_teams + lane) * share;
-        int left = lane < n_teams && from < total ? (int)min(share, total - from) : 0;
-        bool bad = false;
-        const int page = a.kc.page, shift = 31 - __clz(page);
-        StepLoad d0, d1;
-        Place pl = {0, 0, 0, 0, 0};
-        int to_load = left;
-        // pages of the next step that has none yet
-        auto load_pages = [&](StepLoad &d) {
-            d.pg[0] = d.pg[1] = -1;
-            if (to_load == 0) return;
-            if (pl.s == pl.n_steps) next_pair(a, pl);
-            d.p = pl;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = pl.s * kStep + i * 16;
-                if (tok < pl.len) d.pg[i] = __ldg(a.table + (size_t)pl.b * a.table_cap + (tok >> shift));
-            }
-            ++pl.s;
-            --to_load;
-        };
-        auto load_scales = [&](StepLoad &d) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                d.ks[i] = d.vs[i] = 0.f;
-                const bool ok = (unsigned)d.pg[i] < (unsigned)a.kc.n_pages;
-                if (ok) {
-                    d.ks[i] = __ldg(a.kc.k_scale + (size_t)d.pg[i] * Hkv + d.p.h);
-                    d.vs[i] = __ldg(a.kc.v_scale + (size_t)d.pg[i] * Hkv + d.p.h);
-                }
-            }
-        };
-        if (left > 0) {
-            int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before `from`
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (before[mid] * Hkv <= from) lo = mid;
-                else hi = mid;
-            }
-            long long pos = from - before[lo] * Hkv;
-            for (int b = lo * per;; ++b) {
-                set_row(a, pl, b);
-                if (pos < (long long)pl.n_steps * Hkv) break;
-                pos -= (long long)pl.n_steps * Hkv;
-            }
-            pl.h = (int)(pos / pl.n_steps);
-            pl.s = (int)(pos % pl.n_steps);
-            load_pages(d0);
-            load_scales(d0);
-            load_pages(d1);
-        }
-        const int st0 = lane * ns;
-        int st = 0;
-        uint32_t parity = 1;  // a fresh barrier passes
-        uint64_t since = global_ns();
-        bool failed = false;
-        while (__any_sync(0xffffffffu, left > 0)) {
-            const bool ready = left > 0 && mbar_test(smem_u32(&empty[st0 + st]), parity);
-            if (ready) {
-                const int tok = d0.p.s * kStep, len = d0.p.len;
-                bool ok[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ok[i] = (unsigned)d0.pg[i] < (unsigned)a.kc.n_pages;
-                    bad |= !ok[i] && tok + i * 16 < len;
-                }
-                StageMeta &m = meta[st0 + st];
-                m.ks[0] = d0.ks[0];
-                m.ks[1] = d0.ks[1];
-                m.vs[0] = d0.vs[0];
-                m.vs[1] = d0.vs[1];
-                m.nv[0] = ok[0] ? min(16, len - tok) : 0;
-                m.nv[1] = ok[1] ? min(16, len - tok - 16) : 0;
-                m.b = d0.p.b;
-                m.h = d0.p.h;
-                m.s = d0.p.s;
-                m.n_steps = d0.p.n_steps;
-                m.len = len;
-                const uint32_t bar = smem_u32(&full[st0 + st]), dst = ring + (uint32_t)(st0 + st) * kStageBytes;
-                if (page >= kStep) {
-                    mbar_expect_tx(bar, ok[0] ? 2 * kStep * kD : 0);
-                    if (ok[0]) {
-                        const int row = (d0.pg[0] * Hkv + d0.p.h) * page + (tok & (page - 1));
-                        tma_rows(dst, &map_k, row, bar);
-                        tma_rows(dst + kStep * kD, &map_v, row, bar);
-                    }
-                } else {
-                    mbar_expect_tx(bar, (ok[0] + ok[1]) * 2 * 16 * kD);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (ok[i]) {
-                            const int row = (d0.pg[i] * Hkv + d0.p.h) * 16;
-                            tma_rows(dst + i * 16 * kD, &map_k, row, bar);
-                            tma_rows(dst + (kStep + i * 16) * kD, &map_v, row, bar);
-                        }
-                }
-                --left;
-                if (++st == ns) {
-                    st = 0;
-                    parity ^= 1;
-                }
-                d0 = d1;
-                load_scales(d0);
-                load_pages(d1);
-            }
-            if (__any_sync(0xffffffffu, ready)) {
-                since = global_ns();
-            } else {
-                __nanosleep(40);
-                if (global_ns() - since > 1000000000ull) {
-                    failed = true;
-                    break;
-                }
-            }
-        }
-        if (bad) atomicOr(a.ws, kDevBadArg);
-        if (failed) {
-            // some consumer gave up; let the copies in flight land before the CTA's memory goes away
-            if (lane == 0) atomicOr(a.ws, kDevTimeout);
-            if (lane < n_teams)
-                for (int i = 0; i < ns; ++i) {
-                    const int u = (st + i) % ns;  // its last use had this parity (of a stage never used, 1: passes)
-                    mbar_wait_bounded(smem_u32(&full[st0 + u]), st + i < ns ? parity : parity ^ 1u);
-                }
-        }
-        return;
-    }
-
-    // ---- consumers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AtGeom<kNT>::kRegsConsumer));
-    if (team >= n_teams) return;  // warps that make no whole team
-    const long long tm = (long long)blockIdx.x * n_teams + team;
-    const long long from = tm * share;
-    if (from >= total) return;
-    const int steps = (int)min(share, total - from);
+    const int total = uniform(before[kAtThreads] * Hkv);
+    const int cta_share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinCtaSteps);
+    const int share = (cta_share + n_teams - 1) / n_teams;
+    const int cta_from = (int)min((long long)blockIdx.x * cta_share, (long long)total);
+    const int cta_steps = min(cta_share, total - cta_from);
+    const int from = cta_from + team * share;
+    // teams without steps (and warps that make no whole team) only help to merge
+    const int steps = team < n_teams ? max(0, min(share, cta_steps - team * share)) : 0;
+    const int tm = blockIdx.x * n_teams + team;
     const int st0 = team * ns;
     const uint32_t base = ring + (uint32_t)st0 * kStageBytes;
+    // the pair and step at a place of the line
+    auto find = [&](int at, Place &p) {
+        int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before it
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] * Hkv <= at) lo = mid;
+            else hi = mid;
+        }
+        int pos = at - before[lo] * Hkv;
+#pragma unroll 1
+        for (int b = lo * per;; ++b) {
+            set_row(a, p, b);
+            if (pos < p.n_steps * Hkv) break;
+            pos -= p.n_steps * Hkv;
+        }
+        p.h = pos / p.n_steps;
+        p.s = pos - p.h * p.n_steps;
+    };
 
+    // ---- the team's first warp keeps its part of the ring full
+    Batch cur = {}, nxt = {};
+    Place pl = {};                                   // the first step not yet in a batch
+    int to_load = steps, to_issue = steps, in_cur = 0;  // steps in no batch, steps not issued, place in cur
+    bool bad = false;
+    auto fetch = [&]() {
+        nxt.n = 0;
+        if (to_load == 0) return;
+        if (pl.s == pl.n_steps) next_pair(a, pl);
+        const int n = min(min(16, pl.n_steps - pl.s), to_load);
+        load_batch(a, pl, n, nxt, &bad);
+        pl.s += n;
+        to_load -= n;
+    };
+    auto issue = [&](int st) {  // the next step into stage st
+        if (in_cur == cur.n) {
+            cur = nxt;
+            in_cur = 0;
+            fetch();
+        }
+        const int page = opaque(a.kc.page), tok = (cur.p.s + in_cur) * kStep, len = cur.p.len;
+        // lane i < 2: half i
+        const int src = (2 * in_cur + (lane & 1)) & 31;
+        const int pg = __shfl_sync(0xffffffffu, cur.pg, src);
+        const float ks = __shfl_sync(0xffffffffu, cur.ks, src), vs = __shfl_sync(0xffffffffu, cur.vs, src);
+        const uint32_t bar = smem_u32(&full[st0 + st]);
+        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 3u;
+        StageMeta &m = meta[st0 + st];
+        if (lane < 2) {
+            m.ks[lane] = ks;
+            m.vs[lane] = vs;
+            m.nv[lane] = pg >= 0 ? min(16, len - tok - lane * 16) : 0;
+        } else if (lane == 2) {
+            m.b = cur.p.b;
+            m.h = cur.p.h;
+            m.s = cur.p.s + in_cur;
+            m.n_steps = cur.p.n_steps;
+            m.len = len;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar, page >= kStep ? (have & 1u) * 2 * kStep * kD : __popc(have) * 2 * 16 * kD);
+        __syncwarp();
+        const uint32_t dst = base + (uint32_t)st * kStageBytes;
+        if (page >= kStep) {
+            if (lane == 0 && pg >= 0) {
+                const int row = (pg * Hkv + cur.p.h) * page + (tok & (page - 1));
+                tma_rows(dst, &map_k, row, bar);
+                tma_rows(dst + kStep * kD, &map_v, row, bar);
+            }
+        } else if (lane < 2 && pg >= 0) {
+            const int row = (pg * Hkv + cur.p.h) * 16;
+            tma_rows(dst + lane * 16 * kD, &map_k, row, bar);
+            tma_rows(dst + (kStep + lane * 16) * kD, &map_v, row, bar);
+        }
+        ++in_cur;
+        --to_issue;
+    };
+    if (wt == 0 && steps > 0) {
+        // odd lanes look up the last step: first and last pair are for the merge
+        Place p;
+        const int at = from + (lane & 1) * (steps - 1);
+        find(at, p);
+        if (lane < 2) {
+            const int x0 = at - p.s, x1 = x0 + p.n_steps - 1;  // the pair's own steps
+            const int c0 = x0 / cta_share, c1 = x1 / cta_share;
+            stretch[team].pair[lane] = p.b * Hkv + p.h;
+            stretch[team].t0[lane] = c0 * n_teams + (x0 - c0 * cta_share) / share;
+            stretch[team].t1[lane] = c1 * n_teams + (x1 - c1 * cta_share) / share;
+        }
+        pl.b = uniform(p.b);  // lane 0's
+        pl.h = uniform(p.h);
+        pl.s = uniform(p.s);
+        pl.len = uniform(p.len);
+        pl.n_steps = uniform(p.n_steps);
+        fetch();
+        cur = nxt;
+        fetch();
+    }
+
+    // ---- all warps of the team consume
     uint32_t qh[kQ][kN][16];      // B fragments of the queries
     float qf[kN][2];              // score factor of rows 2c, 2c + 1
     int lim[kN][2];               // the last token they see
@@ -400,8 +464,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     auto begin_pair = [&](const StageMeta &mt) {
         b = mt.b;
         h = mt.h;
-        nn = a.n_new ? min(max(__ldg(a.n_new + b), 0), a.n_q) : a.n_q;
-        first_full = mt.len - nn + 1;  // tokens below this are seen by every query
+        nn = opaque(a.n_new != nullptr) ? min(max(__ldg(a.n_new + b), 0), a.n_q) : a.n_q;
+        first_full = uniform(mt.len - nn + 1);  // tokens below this are seen by every query
         starts_pair = mt.s == 0;
         E_top = exp2_int(-100);
         E_inv = exp2_int(100 + kPScale);
@@ -496,21 +560,30 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         }
     };
 
-    int st = 0;
+    // One loop fills the ring (it < 0), consumes the steps, and ends the last
+    // pair (it == steps): each part of the code stands once, because every CTA
+    // fetches all of it (this loop unrolled by hand took 12 us more).
+    int st = 0, put = 0;  // stages: next to consume, next to fill
     uint32_t parity = 0;
-    for (int it = 0; it < steps; ++it) {
-        if (!mbar_wait_bounded(smem_u32(&full[st0 + st]), parity)) {
-            if (lane == 0) atomicOr(a.ws, kDevTimeout);
-            return;
+    bool failed = false;
+#pragma unroll 1
+    for (int it = steps > 0 ? -ns : 1; it <= steps; ++it) {
+        if (it >= 0) {
+        StageMeta mt;
+        if (it < steps) {
+            // a wait that ran out does not leave the loop (lanes would part there):
+            // the rest is computed from what the stages hold, and thrown away
+            if (!failed) failed = !wait_warp(smem_u32(&full[st0 + st]), parity);
+            mt = meta[st0 + st];
         }
-        const StageMeta mt = meta[st0 + st];
-        if (mt.b != b || mt.h != h) {
-            if (b >= 0) end_pair();
+        if (it == steps || uniform(mt.b != b || mt.h != h)) {
+            if (uniform(b >= 0) && !failed) end_pair();
+            if (it == steps) break;
             begin_pair(mt);
         }
         ends_pair = mt.s + 1 == mt.n_steps;
         const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
-        const int t0 = mt.s * kStep;
+        const int t0 = uniform(mt.s) * kStep;
 
         // scores
         float s[kN][2][4];
@@ -539,7 +612,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             }
         }
         // places without a token and tokens behind a query's own
-        const bool edge = mt.nv[0] < 16 || mt.nv[1] < 16 || t0 + kStep > first_full;
+        const bool holes = uniform(mt.nv[0] < 16 || mt.nv[1] < 16);
+        const bool edge = holes || t0 + kStep > first_full;
         bool hide = false;
         if (edge) {
 #pragma unroll
@@ -553,7 +627,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     }
             // Places without a token may hold anything, NaN codes too: their
             // values become zeros before the second product meets them.
-            if (mt.nv[0] < 16 || mt.nv[1] < 16) {
+            if (holes) {
+#pragma unroll 1
                 for (int i = lane; i < kStep * 8; i += 32) {
                     const int row = i >> 3;
                     if ((row & 15) >= (row < 16 ? mt.nv[0] : mt.nv[1]))
@@ -566,10 +641,10 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             // A token that some of the queries do not see takes part in the second
             // product with p = 0 for them: where its value is NaN, the queries that
             // see it get their NaN here and the product a zero.
-            if (kType == SPARK_KV8_E4M3 && a.n_q > 1) {
+            if (kType == SPARK_KV8_E4M3 && opaque(a.n_q) > 1) {
 #pragma unroll 1
                 for (int i = max(first_full - t0, 0); i < kStep; ++i) {
-                    if ((i & 15) >= (i < 16 ? mt.nv[0] : mt.nv[1])) continue;
+                    // (places without a token are zeros by now)
                     const uint4 w = lds128(vb + (uint32_t)i * kD + ((uint32_t)(g ^ (i & 7)) << 4));
                     const uint32_t ww[4] = {nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w)};
                     if (!__any_sync(0xffffffffu, (ww[0] | ww[1] | ww[2] | ww[3]) != 0)) continue;
@@ -691,69 +766,153 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 }
             }
         }
-        // the stage is free once every warp of the team has read it
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
+        if (opaque(tw) > 1 && lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
         if (++st == ns) {
             st = 0;
             parity ^= 1;
         }
+        }
+        // A stage is free once every warp of the team has read it.  A team of
+        // one refills it at once; a larger one refills the stage before, which
+        // its other warps have most likely left.
+        if (opaque(wt) == 0 && to_issue > 0 && !failed && (it != 0 || opaque(tw) == 1)) {
+            if (opaque(tw) > 1 && it > 0) {
+                // `put` was consumed a step ago, in the lap before this one's unless it has wrapped since
+                failed = !wait_warp(smem_u32(&empty[st0 + put]), st > put ? parity : parity ^ 1u);
+            }
+            if (!failed) issue(put);
+            if (++put == ns) put = 0;
+        }
     }
-    end_pair();
-}
+    if (failed) {
+        if (lane == 0) atomicOr(a.ws, kDevTimeout);
+        // let the copies in flight land before the CTA's memory goes away
+        if (wt == 0) {
+#pragma unroll 1
+            for (int i = 0; i < 2 * ns; ++i) wait_warp(smem_u32(&full[st0 + i / 2]), (uint32_t)(i & 1));
+        }
+    }
+    if (bad) atomicOr(a.ws, kDevBadArg);
 
-// Merge of the partials of one query row: CTA = row, warps take partials in
-// turn, and their results are added in warp order.
-constexpr int kMgWarps = 8;
+    // ---- rows without tokens: zeros
+#pragma unroll 1
+    for (int r = blockIdx.x * kAtWarps + warp; r < a.B; r += gridDim.x * kAtWarps) {
+        if (clamped_len(a, r) > 0) continue;
+        const int n = a.n_new ? min(max(__ldg(a.n_new + r), 0), a.n_q) : a.n_q;
+        float4 *dst = reinterpret_cast<float4 *>(a.out + (size_t)r * Hkv * a.rows * kD);
+#pragma unroll 1
+        for (int i = 0; i < Hkv * a.rows; ++i)
+            if (i % a.rows % a.n_q < n) dst[(size_t)i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 
-__global__ void __launch_bounds__(kMgWarps * 32) attn_kv8_merge_kernel(const AttnArgs a) {
-    __shared__ float4 acc_s[kMgWarps][32];
-    __shared__ float m_s[kMgWarps], l_s[kMgWarps];
-    const long bh = blockIdx.x / a.rows;
-    const int row = blockIdx.x % a.rows, b = (int)(bh / a.kc.Hkv), h = (int)(bh % a.kc.Hkv);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nn = a.n_new ? min(max(__ldg(a.n_new + b), 0), a.n_q) : a.n_q;
-    if (row % a.n_q >= nn) return;
-    float *out = a.out + (bh * a.rows + row) * kD;
-    const int n_steps = (clamped_len(a, b) + kStep - 1) / kStep;
-    if (n_steps == 0) {
-        if (warp == 0) *reinterpret_cast<float4 *>(out + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-        return;
+    // ---- pairs that several teams share.  Lane t of every warp looks at team
+    // t's first and last pair; the first team of this CTA that has steps of a
+    // pair stands for it.
+    __syncthreads();
+    const int cta0 = blockIdx.x * n_teams, cta_end = cta0 + n_teams;
+    const int n_act = (cta_steps + share - 1) / share;
+    bool job[2] = {false, false}, cross[2] = {false, false};
+    Stretch mine = {};
+    if (lane < n_act) {
+        mine = stretch[lane];
+        job[0] = mine.t0[0] != mine.t1[0] && (lane == 0 || mine.t0[0] == cta0 + lane);
+        job[1] = mine.t0[1] != mine.t1[1] && mine.pair[1] != mine.pair[0];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) cross[i] = job[i] && (mine.t0[i] < cta0 || mine.t1[i] >= cta_end);
     }
-    const long long share = a.layout[0], first = a.layout[1 + b] * a.kc.Hkv + (long long)h * n_steps;
-    const long long t0 = first / share, t1 = (first + n_steps - 1) / share;
-    if (t0 == t1) return;  // written by the one team that had it all
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long t = t0 + warp; t <= t1; t += kMgWarps) {
-        const size_t at = (size_t)(t + bh) * a.rows + row;
-        const float2 x = *reinterpret_cast<const float2 *>(a.ml + at * 2);
-        const float4 v = *reinterpret_cast<const float4 *>(a.acc + at * kD + lane * 4);
-        const float mn = fmaxf(m, x.x);
-        const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn), e = mn == -INFINITY ? 1.f : exp2_approx(x.x - mn);
-        l = l * f + x.y * e;
-        acc = make_float4(acc.x * f + v.x * e, acc.y * f + v.y * e, acc.z * f + v.z * e, acc.w * f + v.w * e);
-        m = mn;
+    int turn = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll 1
+        for (uint32_t todo = __ballot_sync(0xffffffffu, i ? job[1] : job[0]); todo; todo &= todo - 1) {
+            const int t = __ffs(todo) - 1;
+            const int pair = __shfl_sync(0xffffffffu, i ? mine.pair[1] : mine.pair[0], t);
+            const int t1 = __shfl_sync(0xffffffffu, i ? mine.t1[1] : mine.t1[0], t);
+            const bool out_too = __shfl_sync(0xffffffffu, (int)!(i ? cross[1] : cross[0]), t) != 0;
+            const int n = uniform(a.n_new ? min(max(__ldg(a.n_new + pair / Hkv), 0), a.n_q) : a.n_q);
+#pragma unroll 1
+            for (int row = 0; row < a.rows; ++row) {
+                if (row % a.n_q >= n) continue;
+                if (turn++ % kAtWarps != warp) continue;
+                const size_t at = (size_t)(cta0 + t + pair) * a.rows + row;
+                const Merged r = merge_partials(a.acc + at * kD, a.ml + at * 2, min(t1 + 1, cta_end) - (cta0 + t),
+                                                a.rows);
+                if (out_too) {
+                    write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
+                } else {
+                    const size_t to = (size_t)(blockIdx.x + pair) * a.rows + row;
+                    __stcg(reinterpret_cast<float4 *>(a.acc_c + to * kD) + lane, r.acc);
+                    if (lane == 0) __stcg(reinterpret_cast<float2 *>(a.ml_c + to * 2), make_float2(r.m, r.l));
+                }
+            }
+        }
     }
-    acc_s[warp][lane] = acc;
-    if (lane == 0) {
-        m_s[warp] = m;
-        l_s[warp] = l;
+
+    // ---- pairs that several CTAs share (at most this CTA's first and last):
+    // the last of them to get here merges the CTAs' partials, in their order.
+    // A boundary between CTAs lies in one pair, so the first CTA numbers it.
+    __threadfence();
+    __syncthreads();
+    if (warp == 0) {
+        if (lane < 2) last_pair[lane] = -1;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!cross[i]) continue;
+            const int c0 = mine.t0[i] / n_teams, c1 = mine.t1[i] / n_teams;
+            const uint32_t seen = atomicAdd(a.counter + c0, 1u);
+            if (seen == (uint32_t)(c1 - c0)) {
+                a.counter[c0] = 0;  // as the next call needs it
+                const int k = c0 < (int)blockIdx.x ? 0 : 1;  // the CTA's first pair, or its last
+                last_c0[k] = c0;
+                last_c1[k] = c1;
+                last_pair[k] = mine.pair[i];
+            }
+        }
+        __threadfence();
     }
     __syncthreads();
-    if (warp) return;
-    m = -INFINITY;
-    for (int i = 0; i < kMgWarps; ++i) m = fmaxf(m, m_s[i]);
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < kMgWarps; ++i) {
-        const float e = m == -INFINITY ? 1.f : exp2_approx(m_s[i] - m);
-        const float4 v = acc_s[i][lane];
-        l += l_s[i] * e;
-        acc = make_float4(acc.x + v.x * e, acc.y + v.y * e, acc.z + v.z * e, acc.w + v.w * e);
+    const int parts = max(1, kAtWarps / a.rows);
+    float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + 64 * kD;  // at most 64 (row, part)s
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int pair = uniform(last_pair[k]);
+        if (pair < 0) continue;
+        const int c0 = uniform(last_c0[k]), n = uniform(last_c1[k]) - c0 + 1, each = (n + parts - 1) / parts;
+        const int nn_p = uniform(a.n_new ? min(max(__ldg(a.n_new + pair / Hkv), 0), a.n_q) : a.n_q);
+#pragma unroll 1
+        for (int it = warp; it < a.rows * parts; it += kAtWarps) {
+            const int row = it / parts, i0 = it % parts * each;
+            if (row % a.n_q >= nn_p) continue;
+            const size_t at = (size_t)(c0 + i0 + pair) * a.rows + row;
+            const Merged r = merge_partials(a.acc_c + at * kD, a.ml_c + at * 2, max(0, min(each, n - i0)), a.rows);
+            if (parts == 1) {
+                write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
+            } else {
+                reinterpret_cast<float4 *>(sm_acc + it * kD)[lane] = r.acc;
+                if (lane == 0) reinterpret_cast<float2 *>(sm_ml)[it] = make_float2(r.m, r.l);
+            }
+        }
+        if (parts == 1) continue;
+        __syncthreads();
+#pragma unroll 1
+        for (int row = warp; row < a.rows; row += kAtWarps) {
+            if (row % a.n_q >= nn_p) continue;
+            Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+            for (int i = 0; i < parts; ++i) r.m = fmaxf(r.m, sm_ml[(row * parts + i) * 2]);
+#pragma unroll 1
+            for (int i = 0; i < parts; ++i) {
+                const float e = r.m == -INFINITY ? 1.f : exp2_approx(sm_ml[(row * parts + i) * 2] - r.m);
+                const float4 v = reinterpret_cast<const float4 *>(sm_acc + (row * parts + i) * kD)[lane];
+                r.l += sm_ml[(row * parts + i) * 2 + 1] * e;
+                r.acc = make_float4(r.acc.x + v.x * e, r.acc.y + v.y * e, r.acc.z + v.z * e, r.acc.w + v.w * e);
+            }
+            write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
+        }
+        __syncthreads();
     }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<float4 *>(out + lane * 4) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 }
 
 template <typename E, int kType, int kNT>
@@ -795,9 +954,14 @@ cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, 
     a.out = out;
     char *w = static_cast<char *>(ws);
     a.ws = reinterpret_cast<uint32_t *>(w);
-    a.layout = reinterpret_cast<long long *>(w + kWsHeader);
-    a.acc = reinterpret_cast<float *>(w + kWsHeader + attn_layout_bytes(B));
-    a.ml = a.acc + (size_t)attn_slots(B, kc.Hkv, num_sms) * a.rows * kD;
+    a.counter = reinterpret_cast<uint32_t *>(w + kWsHeader);
+    const long pairs = (long)B * kc.Hkv;
+    const size_t team_rows = (size_t)attn_team_slots(pairs, num_sms) * a.rows;
+    const size_t cta_rows = (size_t)(num_sms + pairs) * a.rows;
+    a.acc = reinterpret_cast<float *>(w + kWsHeader + attn_counter_bytes(num_sms));
+    a.acc_c = a.acc + team_rows * kD;
+    a.ml = a.acc_c + cta_rows * kD;
+    a.ml_c = a.ml + team_rows * 2;
     CUtensorMap mk, mv;
     const long rows = (long)kc.n_pages * kc.Hkv * kc.page;
     // a pool without pages is never read: any address does
@@ -805,16 +969,11 @@ cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, 
         !make_kv8_map(&mv, rows ? kc.v : ws, rows ? rows : 1, kc.page < kStep ? kc.page : kStep))
         return cudaErrorInvalidValue;
     const bool e4 = kc.type == SPARK_KV8_E4M3;
-    cudaError_t e;
     if (dtype == SPARK_F32)
-        e = e4 ? launch_rows<float, SPARK_KV8_E4M3>(mk, mv, q, a, num_sms, st)
-               : launch_rows<float, SPARK_KV8_I8>(mk, mv, q, a, num_sms, st);
-    else
-        e = e4 ? launch_rows<__nv_bfloat16, SPARK_KV8_E4M3>(mk, mv, q, a, num_sms, st)
-               : launch_rows<__nv_bfloat16, SPARK_KV8_I8>(mk, mv, q, a, num_sms, st);
-    if (e != cudaSuccess) return e;
-    attn_kv8_merge_kernel<<<(unsigned)((long)B * kc.Hkv * a.rows), kMgWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+        return e4 ? launch_rows<float, SPARK_KV8_E4M3>(mk, mv, q, a, num_sms, st)
+                  : launch_rows<float, SPARK_KV8_I8>(mk, mv, q, a, num_sms, st);
+    return e4 ? launch_rows<__nv_bfloat16, SPARK_KV8_E4M3>(mk, mv, q, a, num_sms, st)
+              : launch_rows<__nv_bfloat16, SPARK_KV8_I8>(mk, mv, q, a, num_sms, st);
 }
 
 }  // namespace spark

@@ -493,8 +493,8 @@ SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t s
  * pages hold, taken outside [0, n_pages], a page number outside the pool)
  * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
  * Requires B * table_cap + n_pages < 2^31 and table_cap * page < 2^31.
- * Workspace: 256 bytes, zero before first use, not shared with a call that
- * may run at the same time (this holds for every workspace of the library).
+ * Workspace: 256 bytes, all zero before first use, not shared with a call
+ * that may run at the same time (this holds for every workspace of the library).
  * B = 0 launches nothing and leaves taken_out as it is.
  */
 SPARK_API int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
@@ -557,10 +557,13 @@ SPARK_API int spark_kv8_append(const void *k_new, const void *v_new, int B, int 
  * with fp32 products' sums and statistics; a query that sees no token gets
  * zeros, and the rows of queries i >= n_new[b] are left as they are.  What
  * the pages hold past lens[b], and table entries past it, is never used.
- * Requires 1 <= G * n_q <= 64.  Lengths out of range (lens past table_cap
+ * Requires 1 <= G * n_q <= 64, finite scales that are not negative, and
+ * B * Hkv * table_cap * page < 2^36.  Lengths out of range (lens past table_cap
  * pages, n_new outside [0, n_q]) are clamped and page numbers outside the
  * pool make their tokens unseen; both raise SPARK_ERR_ARG in the device
- * status word.  Workspace: spark_workspace_bytes_kv8(B, Hkv, G, n_q).
+ * status word.  Workspace: spark_workspace_bytes_kv8(B, Hkv, G, n_q), all
+ * zero before first use; calls of other shapes may use it afterwards as it
+ * is (after SPARK_ERR_TIMEOUT it must be zeroed again).
  * Results do not depend on timing: the same call gives the same bits.
  */
 SPARK_API int spark_decode_attn_kv8(const void *q, int dtype, const spark_kv8cache *kc, const int32_t *table,
