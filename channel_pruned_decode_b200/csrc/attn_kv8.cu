@@ -177,7 +177,7 @@ struct Place {
 struct AttnArgs {
     spark_kv8cache kc;
     const int32_t *table, *lens, *n_new;
-    int table_cap, B, rows, n_q, team_warps, n_stages;
+    int table_cap, B, rows, G, n_q, team_warps, n_stages;
     float *out;
     uint32_t *ws, *counter;
     float *acc, *ml;        // team partials
@@ -234,49 +234,34 @@ __device__ __forceinline__ void load_batch(const AttnArgs &a, const Place &p, in
     }
 }
 
-// The first and the last pair of a team's stretch: number, and the first and
-// last team (counted over all CTAs) that have steps of it.
+// The first and the last pair of a team's stretch: number, place of its first
+// step on the line, steps, and queries.
 struct Stretch {
-    int pair[2], t0[2], t1[2];
+    int pair[2], x0[2], n[2], nn[2];
 };
 
-// What is left of `n` partials of one query row, read as (acc, ml) at stride
-// `rows`: lane i gets channels 4i .. 4i + 3 of acc = sum 2^(m_i - m) acc_i,
-// and m, l.  n <= 32 at a time; partials written by other CTAs are read past L1.
+// Partials (m, l, acc) of one query row put together: acc = sum 2^(m_i - m)
+// acc_i, l likewise.  Lane i has channels 4i .. 4i + 3.
 struct Merged {
     float m, l;
     float4 acc;
 };
 
-__device__ __forceinline__ Merged merge_partials(const float *acc, const float *ml, int n, int rows) {
-    const int lane = threadIdx.x & 31;
-    Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int k = min(32, n - i0);
-        float2 x = make_float2(-INFINITY, 0.f);
-        if (lane < k) x = __ldcg(reinterpret_cast<const float2 *>(ml + (size_t)(i0 + lane) * rows * 2));
-        float m = x.x;
+__device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float w) {
+    acc = make_float4(acc.x + v.x * w, acc.y + v.y * w, acc.z + v.z * w, acc.w + v.w * w);
+}
+
+// Weights of up to 32 partials, lane i's in lane i (x: its m and l; without any
+// seen token every weight is 1, of zeros).  Sets m and l of all of them.
+__device__ __forceinline__ float merge_weights(const float2 &x, Merged &r) {
+    r.m = x.x;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        m = fmaxf(m, r.m);
-        // without any seen token every weight is 1 (of zeros)
-        const float e = m == -INFINITY ? 1.f : exp2_approx(x.x - m), old = m == -INFINITY ? 1.f : exp2_approx(r.m - m);
-        float l = x.y * e;
+    for (int d = 16; d; d >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, d));
+    const float e = r.m == -INFINITY ? 1.f : exp2_approx(x.x - r.m);
+    r.l = x.y * e;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        r.l = r.l * old + l;
-        r.acc = make_float4(r.acc.x * old, r.acc.y * old, r.acc.z * old, r.acc.w * old);
-        r.m = m;
-        const float *at = acc + (size_t)i0 * rows * kD + lane * 4;
-#pragma unroll 4
-        for (int i = 0; i < k; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + (size_t)i * rows * kD));
-            const float w = __shfl_sync(0xffffffffu, e, i);
-            r.acc = make_float4(r.acc.x + v.x * w, r.acc.y + v.y * w, r.acc.z + v.z * w, r.acc.w + v.w * w);
-        }
-    }
-    return r;
+    for (int d = 16; d; d >>= 1) r.l += __shfl_xor_sync(0xffffffffu, r.l, d);
+    return e;
 }
 
 __device__ __forceinline__ void write_row(float *out, const Merged &r) {
@@ -301,7 +286,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ StageMeta meta[kMaxStages];
     __shared__ Stretch stretch[kMaxTeams];
-    __shared__ int last_c0[2], last_c1[2], last_pair[2];  // pairs that this CTA is the last to finish
+    __shared__ int last_c0[2], last_c1[2], last_nn[2], last_pair[2];  // pairs that this CTA is the last to finish
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
     const int tw = a.team_warps, n_teams = kAtWarps / tw, team = warp / tw, wt = warp % tw;
@@ -330,6 +315,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (lane >= d) v += y;
         }
         if (lane == 31) wsum[warp] = v;
+        if (tid < kMaxTeams) stretch[tid].pair[0] = stretch[tid].pair[1] = -1;
         if (tid < kMaxStages) {
             mbar_init(smem_u32(&full[tid]), 1);
             mbar_init(smem_u32(&empty[tid]), tw);
@@ -354,26 +340,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     const int tm = blockIdx.x * n_teams + team;
     const int st0 = team * ns;
     const uint32_t base = ring + (uint32_t)st0 * kStageBytes;
-    // the pair and step at a place of the line
-    auto find = [&](int at, Place &p) {
-        int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before it
-#pragma unroll 1
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (before[mid] * Hkv <= at) lo = mid;
-            else hi = mid;
-        }
-        int pos = at - before[lo] * Hkv;
-#pragma unroll 1
-        for (int b = lo * per;; ++b) {
-            set_row(a, p, b);
-            if (pos < p.n_steps * Hkv) break;
-            pos -= p.n_steps * Hkv;
-        }
-        p.h = pos / p.n_steps;
-        p.s = pos - p.h * p.n_steps;
-    };
-
     // ---- the team's first warp keeps its part of the ring full
     Batch cur = {}, nxt = {};
     Place pl = {};                                   // the first step not yet in a batch
@@ -392,15 +358,27 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         if (in_cur == cur.n) {
             cur = nxt;
             in_cur = 0;
-            fetch();
         }
         const int page = opaque(a.kc.page), tok = (cur.p.s + in_cur) * kStep, len = cur.p.len;
         // lane i < 2: half i
         const int src = (2 * in_cur + (lane & 1)) & 31;
         const int pg = __shfl_sync(0xffffffffu, cur.pg, src);
-        const float ks = __shfl_sync(0xffffffffu, cur.ks, src), vs = __shfl_sync(0xffffffffu, cur.vs, src);
-        const uint32_t bar = smem_u32(&full[st0 + st]);
+        const uint32_t bar = smem_u32(&full[st0 + st]), dst = base + (uint32_t)st * kStageBytes;
         const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 3u;
+        if (page >= kStep) {
+            if (lane == 0 && pg >= 0) {
+                const int row = (pg * Hkv + cur.p.h) * page + (tok & (page - 1));
+                tma_rows(dst, &map_k, row, bar);
+                tma_rows(dst + kStep * kD, &map_v, row, bar);
+            }
+        } else if (lane < 2 && pg >= 0) {
+            const int row = (pg * Hkv + cur.p.h) * 16;
+            tma_rows(dst + lane * 16 * kD, &map_k, row, bar);
+            tma_rows(dst + (kStep + lane * 16) * kD, &map_v, row, bar);
+        }
+        // the copies are on their way before the scales are waited for; the
+        // barrier cannot complete before its one arrival below
+        const float ks = __shfl_sync(0xffffffffu, cur.ks, src), vs = __shfl_sync(0xffffffffu, cur.vs, src);
         StageMeta &m = meta[st0 + st];
         if (lane < 2) {
             m.ks[lane] = ks;
@@ -415,42 +393,33 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_expect_tx(bar, page >= kStep ? (have & 1u) * 2 * kStep * kD : __popc(have) * 2 * 16 * kD);
-        __syncwarp();
-        const uint32_t dst = base + (uint32_t)st * kStageBytes;
-        if (page >= kStep) {
-            if (lane == 0 && pg >= 0) {
-                const int row = (pg * Hkv + cur.p.h) * page + (tok & (page - 1));
-                tma_rows(dst, &map_k, row, bar);
-                tma_rows(dst + kStep * kD, &map_v, row, bar);
-            }
-        } else if (lane < 2 && pg >= 0) {
-            const int row = (pg * Hkv + cur.p.h) * 16;
-            tma_rows(dst + lane * 16 * kD, &map_k, row, bar);
-            tma_rows(dst + (kStep + lane * 16) * kD, &map_v, row, bar);
-        }
+        // pages and scales of the batch after this one, once this one is under way
+        if (in_cur == (cur.n > 1 ? 1 : 0)) fetch();
         ++in_cur;
         --to_issue;
     };
-    if (wt == 0 && steps > 0) {
-        // odd lanes look up the last step: first and last pair are for the merge
-        Place p;
-        const int at = from + (lane & 1) * (steps - 1);
-        find(at, p);
-        if (lane < 2) {
-            const int x0 = at - p.s, x1 = x0 + p.n_steps - 1;  // the pair's own steps
-            const int c0 = x0 / cta_share, c1 = x1 / cta_share;
-            stretch[team].pair[lane] = p.b * Hkv + p.h;
-            stretch[team].t0[lane] = c0 * n_teams + (x0 - c0 * cta_share) / share;
-            stretch[team].t1[lane] = c1 * n_teams + (x1 - c1 * cta_share) / share;
+    if (wt == 0 && steps > 0) {  // the step where the team starts
+        int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before it
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] * Hkv <= from) lo = mid;
+            else hi = mid;
         }
-        pl.b = uniform(p.b);  // lane 0's
-        pl.h = uniform(p.h);
-        pl.s = uniform(p.s);
-        pl.len = uniform(p.len);
-        pl.n_steps = uniform(p.n_steps);
+        int pos = from - before[lo] * Hkv;
+#pragma unroll 1
+        for (int b = lo * per;; ++b) {
+            set_row(a, pl, b);
+            if (pos < pl.n_steps * Hkv) break;
+            pos -= pl.n_steps * Hkv;
+        }
+        pl.b = uniform(pl.b);
+        pl.len = uniform(pl.len);
+        pl.n_steps = uniform(pl.n_steps);
+        pl.h = uniform(pos / pl.n_steps);
+        pl.s = uniform(pos - pl.h * pl.n_steps);
         fetch();
         cur = nxt;
-        fetch();
     }
 
     // ---- all warps of the team consume
@@ -458,6 +427,14 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     float qf[kN][2];              // score factor of rows 2c, 2c + 1
     int lim[kN][2];               // the last token they see
     float o[kN][8][4], m[kN][2], l[kN][2];
+    int qi[kN][2];                // which of its head's queries they are (n_q: none)
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = wt * kRows + (kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3);
+            qi[t][j] = row < a.rows ? row % a.n_q : a.n_q;
+        }
     float E_top = 1.f, E_inv = 1.f;
     int b = -1, h = 0, nn = 0, first_full = 0;
     bool starts_pair = false, ends_pair = false;
@@ -507,9 +484,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 qf[t][j] = __shfl_sync(0xffffffffu, mine, (2 * c + j) * 4);
-                const int col = kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3;
-                const int row = wt * kRows + col, i = row % a.n_q;
-                lim[t][j] = row < a.rows && i < nn ? mt.len - nn + i : -1;
+                lim[t][j] = qi[t][j] < nn ? mt.len - nn + qi[t][j] : -1;
                 m[t][j] = -INFINITY;
                 l[t][j] = 0.f;
             }
@@ -517,9 +492,13 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
         }
     };
-    auto end_pair = [&]() {
+    auto end_pair = [&](bool last) {
         const long bh = (long)b * Hkv + h;
         const bool whole = starts_pair && ends_pair;
+        // A partial of the stretch's last pair goes to the team's own part of
+        // the ring, which it has read by now; one of its first pair, with others
+        // behind it, to global memory.
+        float *part = reinterpret_cast<float *>(sm_raw + (base - smem_u32(sm_raw)));
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
 #pragma unroll
@@ -540,16 +519,17 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             for (int j = 0; j < 2; ++j) {
                 const int col = kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3;
                 const int row = wt * kRows + col;
-                if ((kNT == 0 && c >= 2) || row >= a.rows || row % a.n_q >= nn) continue;
+                if ((kNT == 0 && c >= 2) || qi[t][j] >= nn) continue;
                 float *dst;
                 float f = E_top * exp2_int(-kPScale);
                 if (whole) {
                     dst = a.out + (bh * a.rows + row) * kD;
                     f = l[t][j] == 0.f ? 0.f : f / l[t][j];
                 } else {
-                    const size_t at = (size_t)(tm + bh) * a.rows + row;
-                    dst = a.acc + at * kD;
-                    if (g == 0) *reinterpret_cast<float2 *>(a.ml + at * 2) = make_float2(m[t][j], l[t][j]);
+                    const size_t at = last ? (size_t)row : (size_t)(tm + bh) * a.rows + row;
+                    dst = (last ? part : a.acc) + at * kD;
+                    float *ml = last ? part + a.rows * kD : a.ml;
+                    if (g == 0) *reinterpret_cast<float2 *>(ml + at * 2) = make_float2(m[t][j], l[t][j]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -576,10 +556,18 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (!failed) failed = !wait_warp(smem_u32(&full[st0 + st]), parity);
             mt = meta[st0 + st];
         }
-        if (it == steps || uniform(mt.b != b || mt.h != h)) {
-            if (uniform(b >= 0) && !failed) end_pair();
+        if (it == steps || (!failed && uniform(mt.b != b || mt.h != h))) {
+            if (it == steps && opaque(tw) > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tw * 32) : "memory");
+            if (uniform(b >= 0) && !failed) end_pair(it == steps);
             if (it == steps) break;
             begin_pair(mt);
+            if (wt == 0 && lane == 0) {  // for the merge
+                const int i = it == 0 ? 0 : 1;
+                stretch[team].pair[i] = stretch[team].pair[1] = b * Hkv + h;
+                stretch[team].x0[i] = stretch[team].x0[1] = from + it - mt.s;
+                stretch[team].n[i] = stretch[team].n[1] = mt.n_steps;
+                stretch[team].nn[i] = stretch[team].nn[1] = nn;
+            }
         }
         ends_pair = mt.s + 1 == mt.n_steps;
         const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
@@ -813,37 +801,69 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     const int cta0 = blockIdx.x * n_teams, cta_end = cta0 + n_teams;
     const int n_act = (cta_steps + share - 1) / share;
     bool job[2] = {false, false}, cross[2] = {false, false};
-    Stretch mine = {};
+    // first and last team of the pairs (counted over all CTAs), their numbers and queries
+    int t0[2] = {0, 0}, t1[2] = {0, 0}, pr[2] = {-1, -1}, qn[2] = {0, 0};
     if (lane < n_act) {
-        mine = stretch[lane];
-        job[0] = mine.t0[0] != mine.t1[0] && (lane == 0 || mine.t0[0] == cta0 + lane);
-        job[1] = mine.t0[1] != mine.t1[1] && mine.pair[1] != mine.pair[0];
+        const Stretch x = stretch[lane];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) cross[i] = job[i] && (mine.t0[i] < cta0 || mine.t1[i] >= cta_end);
+        for (int i = 0; i < 2; ++i) {
+            const int x1 = x.x0[i] + x.n[i] - 1, c0 = x.x0[i] / cta_share, c1 = x1 / cta_share;
+            t0[i] = c0 * n_teams + (x.x0[i] - c0 * cta_share) / share;
+            t1[i] = c1 * n_teams + (x1 - c1 * cta_share) / share;
+            pr[i] = x.pair[i];
+            qn[i] = x.nn[i];
+        }
+        job[0] = pr[0] >= 0 && t0[0] != t1[0] && (lane == 0 || t0[0] == cta0 + lane);
+        job[1] = pr[1] >= 0 && t0[1] != t1[1] && pr[1] != pr[0];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) cross[i] = job[i] && (t0[i] < cta0 || t1[i] >= cta_end);
     }
     int turn = 0;
+    bool wrote = false;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
 #pragma unroll 1
         for (uint32_t todo = __ballot_sync(0xffffffffu, i ? job[1] : job[0]); todo; todo &= todo - 1) {
             const int t = __ffs(todo) - 1;
-            const int pair = __shfl_sync(0xffffffffu, i ? mine.pair[1] : mine.pair[0], t);
-            const int t1 = __shfl_sync(0xffffffffu, i ? mine.t1[1] : mine.t1[0], t);
+            const int pair = __shfl_sync(0xffffffffu, i ? pr[1] : pr[0], t);
+            const int te = min(__shfl_sync(0xffffffffu, i ? t1[1] : t1[0], t) - cta0, n_act - 1);  // its last team here
             const bool out_too = __shfl_sync(0xffffffffu, (int)!(i ? cross[1] : cross[0]), t) != 0;
-            const int n = uniform(a.n_new ? min(max(__ldg(a.n_new + pair / Hkv), 0), a.n_q) : a.n_q);
+            // the last team's partial lies in global memory where other pairs follow in its stretch
+            const bool far = __shfl_sync(0xffffffffu, pr[1], te) != pair;
+            const int n = __shfl_sync(0xffffffffu, i ? qn[1] : qn[0], t);
 #pragma unroll 1
-            for (int row = 0; row < a.rows; ++row) {
-                if (row % a.n_q >= n) continue;
-                if (turn++ % kAtWarps != warp) continue;
-                const size_t at = (size_t)(cta0 + t + pair) * a.rows + row;
-                const Merged r = merge_partials(a.acc + at * kD, a.ml + at * 2, min(t1 + 1, cta_end) - (cta0 + t),
-                                                a.rows);
+            for (int row = 0, qx = 0; row < a.rows; ++row, ++qx) {
+                if (qx == a.n_q) qx = 0;
+                if (qx >= n) continue;
+                const bool mine = turn == warp;
+                if (++turn == kAtWarps) turn = 0;
+                if (!mine) continue;
+                const size_t at = (size_t)(cta0 + te + pair) * a.rows + row;
+                const float *part = reinterpret_cast<const float *>(sm_raw + (ring - smem_u32(sm_raw)));
+                const int team_floats = ns * (kStageBytes / 4);
+                float4 vf = make_float4(0.f, 0.f, 0.f, 0.f);
+                float2 x = make_float2(-INFINITY, 0.f);
+                if (far) vf = __ldcg(reinterpret_cast<const float4 *>(a.acc + at * kD) + lane);
+                if (lane <= te - t && !(far && lane == te - t))
+                    x = *reinterpret_cast<const float2 *>(part + (t + lane) * team_floats + a.rows * kD + row * 2);
+                else if (far && lane == te - t)
+                    x = __ldcg(reinterpret_cast<const float2 *>(a.ml + at * 2));
+                Merged r;
+                const float e = merge_weights(x, r);
+                r.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int k = t; k < te + !far; ++k) {
+                    const float4 v = reinterpret_cast<const float4 *>(part + k * team_floats + row * kD)[lane];
+                    add_scaled(r.acc, v, __shfl_sync(0xffffffffu, e, k - t));
+                }
+                if (far) add_scaled(r.acc, vf, __shfl_sync(0xffffffffu, e, te - t));
                 if (out_too) {
                     write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
                 } else {
                     const size_t to = (size_t)(blockIdx.x + pair) * a.rows + row;
                     __stcg(reinterpret_cast<float4 *>(a.acc_c + to * kD) + lane, r.acc);
                     if (lane == 0) __stcg(reinterpret_cast<float2 *>(a.ml_c + to * 2), make_float2(r.m, r.l));
+                    wrote = true;
                 }
             }
         }
@@ -852,7 +872,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     // ---- pairs that several CTAs share (at most this CTA's first and last):
     // the last of them to get here merges the CTAs' partials, in their order.
     // A boundary between CTAs lies in one pair, so the first CTA numbers it.
-    __threadfence();
+    if (wrote) __threadfence();
     __syncthreads();
     if (warp == 0) {
         if (lane < 2) last_pair[lane] = -1;
@@ -860,33 +880,53 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!cross[i]) continue;
-            const int c0 = mine.t0[i] / n_teams, c1 = mine.t1[i] / n_teams;
+            const int c0 = t0[i] / n_teams, c1 = t1[i] / n_teams;
             const uint32_t seen = atomicAdd(a.counter + c0, 1u);
             if (seen == (uint32_t)(c1 - c0)) {
                 a.counter[c0] = 0;  // as the next call needs it
                 const int k = c0 < (int)blockIdx.x ? 0 : 1;  // the CTA's first pair, or its last
                 last_c0[k] = c0;
                 last_c1[k] = c1;
-                last_pair[k] = mine.pair[i];
+                last_nn[k] = qn[i];
+                last_pair[k] = pr[i];
             }
         }
         __threadfence();
     }
     __syncthreads();
-    const int parts = max(1, kAtWarps / a.rows);
+    const int parts = max(1, kAtWarps / a.rows);  // warps per row
     float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + 64 * kD;  // at most 64 (row, part)s
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const int pair = uniform(last_pair[k]);
         if (pair < 0) continue;
         const int c0 = uniform(last_c0[k]), n = uniform(last_c1[k]) - c0 + 1, each = (n + parts - 1) / parts;
-        const int nn_p = uniform(a.n_new ? min(max(__ldg(a.n_new + pair / Hkv), 0), a.n_q) : a.n_q);
+        const int nn_p = uniform(last_nn[k]);
 #pragma unroll 1
         for (int it = warp; it < a.rows * parts; it += kAtWarps) {
-            const int row = it / parts, i0 = it % parts * each;
-            if (row % a.n_q >= nn_p) continue;
-            const size_t at = (size_t)(c0 + i0 + pair) * a.rows + row;
-            const Merged r = merge_partials(a.acc_c + at * kD, a.ml_c + at * 2, max(0, min(each, n - i0)), a.rows);
+            const int row = it / parts, i0 = (it - row * parts) * each, i1 = min(n, i0 + each);
+            if (a.n_q > 1 && row % a.n_q >= nn_p) continue;
+            Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+            for (int i = i0; i < i1; i += 8) {  // 8 at a time, all loads before the weights
+                const size_t at = (size_t)(c0 + i + pair) * a.rows + row, step = a.rows;
+                const int cnt = min(8, i1 - i);
+                float4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = u < cnt ? __ldcg(reinterpret_cast<const float4 *>(a.acc_c + (at + u * step) * kD) + lane)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                float2 x = make_float2(-INFINITY, 0.f);
+                if (lane < cnt) x = __ldcg(reinterpret_cast<const float2 *>(a.ml_c + (at + lane * step) * 2));
+                if (lane == 8) x = make_float2(r.m, r.l);  // what the groups before left
+                const float4 old = r.acc;
+                const float e = merge_weights(x, r);
+                r.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                add_scaled(r.acc, old, __shfl_sync(0xffffffffu, e, 8));
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (u < cnt) add_scaled(r.acc, v[u], __shfl_sync(0xffffffffu, e, u));
+            }
             if (parts == 1) {
                 write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
             } else {
@@ -898,17 +938,15 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         __syncthreads();
 #pragma unroll 1
         for (int row = warp; row < a.rows; row += kAtWarps) {
-            if (row % a.n_q >= nn_p) continue;
-            Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            if (a.n_q > 1 && row % a.n_q >= nn_p) continue;
+            Merged r;
+            const float e = merge_weights(
+                lane < parts ? reinterpret_cast<const float2 *>(sm_ml)[row * parts + lane] : make_float2(-INFINITY, 0.f), r);
+            r.acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int i = 0; i < parts; ++i) r.m = fmaxf(r.m, sm_ml[(row * parts + i) * 2]);
-#pragma unroll 1
-            for (int i = 0; i < parts; ++i) {
-                const float e = r.m == -INFINITY ? 1.f : exp2_approx(sm_ml[(row * parts + i) * 2] - r.m);
-                const float4 v = reinterpret_cast<const float4 *>(sm_acc + (row * parts + i) * kD)[lane];
-                r.l += sm_ml[(row * parts + i) * 2 + 1] * e;
-                r.acc = make_float4(r.acc.x + v.x * e, r.acc.y + v.y * e, r.acc.z + v.z * e, r.acc.w + v.w * e);
-            }
+            for (int i = 0; i < parts; ++i)
+                add_scaled(r.acc, reinterpret_cast<const float4 *>(sm_acc + (row * parts + i) * kD)[lane],
+                           __shfl_sync(0xffffffffu, e, i));
             write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
         }
         __syncthreads();
@@ -950,6 +988,7 @@ cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, 
     a.table_cap = table_cap;
     a.B = B;
     a.rows = G * n_q;
+    a.G = G;
     a.n_q = n_q;
     a.out = out;
     char *w = static_cast<char *>(ws);
