@@ -168,6 +168,17 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
     return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
 }
 
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p) {
+    uint32_t r;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+
+// A kernel launched with programmatic serialisation may start before the one
+// ahead of it has ended; it touches no global memory before this wait.
+__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A place on the line of steps.
 struct Place {
     int b, h, s;       // row, kv head, step of the row
@@ -293,6 +304,15 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     const int Hkv = a.kc.Hkv, ns = a.n_stages;
     const uint32_t ring = (smem_u32(sm_raw) + 1023u) & ~1023u;
 
+    if (tid < kMaxTeams) stretch[tid].pair[0] = stretch[tid].pair[1] = -1;
+    if (tid < kMaxStages) {
+        mbar_init(smem_u32(&full[tid]), 1);
+        mbar_init(smem_u32(&empty[tid]), tw);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    let_next_kernel_start();
+    wait_for_prior_kernel();
+
     // ---- the line: steps before each thread's rows, and in all
     const int per = (a.B + kAtThreads - 1) / kAtThreads;
     {
@@ -315,12 +335,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (lane >= d) v += y;
         }
         if (lane == 31) wsum[warp] = v;
-        if (tid < kMaxTeams) stretch[tid].pair[0] = stretch[tid].pair[1] = -1;
-        if (tid < kMaxStages) {
-            mbar_init(smem_u32(&full[tid]), 1);
-            mbar_init(smem_u32(&empty[tid]), tw);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncthreads();
         int pre = 0;
 #pragma unroll 1
@@ -798,35 +812,34 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     // t's first and last pair; the first team of this CTA that has steps of a
     // pair stands for it.
     __syncthreads();
-    const int cta0 = blockIdx.x * n_teams, cta_end = cta0 + n_teams;
-    const int n_act = (cta_steps + share - 1) / share;
+    const int cta0 = blockIdx.x * n_teams, cta_to = cta_from + cta_steps;
     bool job[2] = {false, false}, cross[2] = {false, false};
-    // first and last team of the pairs (counted over all CTAs), their numbers and queries
-    int t0[2] = {0, 0}, t1[2] = {0, 0}, pr[2] = {-1, -1}, qn[2] = {0, 0};
-    if (lane < n_act) {
+    int pr[2] = {-1, -1}, qn[2] = {0, 0}, x0[2] = {0, 0}, x1[2] = {0, 0};  // the pairs, their queries, first and last step
+    if (lane < n_teams && lane * share < cta_steps) {
         const Stretch x = stretch[lane];
+        const int f = cta_from + lane * share, t = min(f + share, cta_to);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int x1 = x.x0[i] + x.n[i] - 1, c0 = x.x0[i] / cta_share, c1 = x1 / cta_share;
-            t0[i] = c0 * n_teams + (x.x0[i] - c0 * cta_share) / share;
-            t1[i] = c1 * n_teams + (x1 - c1 * cta_share) / share;
             pr[i] = x.pair[i];
             qn[i] = x.nn[i];
+            x0[i] = x.x0[i];
+            x1[i] = x.x0[i] + x.n[i] - 1;
+            job[i] = pr[i] >= 0 && (x0[i] < f || x1[i] >= t);  // others have steps of it
         }
-        job[0] = pr[0] >= 0 && t0[0] != t1[0] && (lane == 0 || t0[0] == cta0 + lane);
-        job[1] = pr[1] >= 0 && t0[1] != t1[1] && pr[1] != pr[0];
+        job[0] = job[0] && (lane == 0 || x0[0] >= f);
+        job[1] = job[1] && pr[1] != pr[0];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) cross[i] = job[i] && (t0[i] < cta0 || t1[i] >= cta_end);
+        for (int i = 0; i < 2; ++i) cross[i] = job[i] && (x0[i] < cta_from || x1[i] >= cta_to);
     }
     int turn = 0;
-    bool wrote = false;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
 #pragma unroll 1
         for (uint32_t todo = __ballot_sync(0xffffffffu, i ? job[1] : job[0]); todo; todo &= todo - 1) {
             const int t = __ffs(todo) - 1;
             const int pair = __shfl_sync(0xffffffffu, i ? pr[1] : pr[0], t);
-            const int te = min(__shfl_sync(0xffffffffu, i ? t1[1] : t1[0], t) - cta0, n_act - 1);  // its last team here
+            // its last team here
+            const int te = 31 - __clz(__ballot_sync(0xffffffffu, pr[0] == pair || pr[1] == pair));
             const bool out_too = __shfl_sync(0xffffffffu, (int)!(i ? cross[1] : cross[0]), t) != 0;
             // the last team's partial lies in global memory where other pairs follow in its stretch
             const bool far = __shfl_sync(0xffffffffu, pr[1], te) != pair;
@@ -863,7 +876,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     const size_t to = (size_t)(blockIdx.x + pair) * a.rows + row;
                     __stcg(reinterpret_cast<float4 *>(a.acc_c + to * kD) + lane, r.acc);
                     if (lane == 0) __stcg(reinterpret_cast<float2 *>(a.ml_c + to * 2), make_float2(r.m, r.l));
-                    wrote = true;
                 }
             }
         }
@@ -872,7 +884,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     // ---- pairs that several CTAs share (at most this CTA's first and last):
     // the last of them to get here merges the CTAs' partials, in their order.
     // A boundary between CTAs lies in one pair, so the first CTA numbers it.
-    if (wrote) __threadfence();
+    // (the barrier and the counter's release and acquire order the partials.)
     __syncthreads();
     if (warp == 0) {
         if (lane < 2) last_pair[lane] = -1;
@@ -880,8 +892,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!cross[i]) continue;
-            const int c0 = t0[i] / n_teams, c1 = t1[i] / n_teams;
-            const uint32_t seen = atomicAdd(a.counter + c0, 1u);
+            const int c0 = x0[i] / cta_share, c1 = x1[i] / cta_share;
+            const uint32_t seen = add_acq_rel(a.counter + c0);
             if (seen == (uint32_t)(c1 - c0)) {
                 a.counter[c0] = 0;  // as the next call needs it
                 const int k = c0 < (int)blockIdx.x ? 0 : 1;  // the CTA's first pair, or its last
@@ -891,7 +903,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 last_pair[k] = pr[i];
             }
         }
-        __threadfence();
     }
     __syncthreads();
     const int parts = max(1, kAtWarps / a.rows);  // warps per row
@@ -960,8 +971,17 @@ static cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, cons
     auto kernel = attn_kv8_kernel<E, kType, kNT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)num_sms, AtGeom<kNT>::kThreads, smem, st>>>(mk, mv, static_cast<const E *>(q), a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)num_sms);
+    cfg.blockDim = dim3(AtGeom<kNT>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mk, mv, static_cast<const E *>(q), a);
 }
 
 template <typename E, int kType>
