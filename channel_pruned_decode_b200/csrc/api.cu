@@ -33,7 +33,7 @@ cudaError_t launch_pages_trim(const int32_t *lens, const int32_t *keep, int B, i
                               const int32_t *taken, const int32_t *table, int table_cap, int32_t *lens_out,
                               int32_t *taken_out, void *ws, cudaStream_t st);
 cudaError_t launch_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype,
-                              const int32_t *slots, const spark_kv8cache &kc, void *ws, cudaStream_t st);
+                              const int32_t *slots, const spark_kv8cache &kc, void *ws, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, const int32_t *table, int table_cap,
                             const int32_t *lens, const int32_t *n_new, int B, int G, int n_q, float *out, void *ws,
                             int num_sms, cudaStream_t st);
@@ -472,13 +472,13 @@ int spark_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int
     if (rc != SPARK_OK) return rc;
     if (B < 0 || n_cap < 0 || elem_size(dtype) == 0) return SPARK_ERR_ARG;
     // 32-bit counts of (row, page-sized piece, head, key or value) and of slots
-    if ((double)B * kc->Hkv * ((n_cap + 15) / 16) * 2 > 2147483647.0 || (double)B * n_cap > 2147483647.0)
+    if ((double)B * kc->Hkv * (n_cap / 16 + 2) * 2 > 2147483647.0 || (double)B * n_cap > 2147483647.0)
         return SPARK_ERR_UNSUPPORTED;
     if ((long)B * kc->Hkv == 0 || n_cap == 0) return SPARK_OK;
     if (!k_new || !v_new || !slots || !aligned16(k_new) || !aligned16(v_new) || !aligned4(slots))
         return SPARK_ERR_ARG;
     if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;
-    cudaError_t e = launch_kv8_append(k_new, v_new, B, n_cap, dtype, slots, *kc, workspace,
+    cudaError_t e = launch_kv8_append(k_new, v_new, B, n_cap, dtype, slots, *kc, workspace, num_sms(),
                                       static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }

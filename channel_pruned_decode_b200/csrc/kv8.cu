@@ -9,10 +9,16 @@
 // value is read once and its code written once.
 #include "kv8.cuh"
 
+#include <algorithm>
+
 namespace spark {
 
-constexpr int kApWarps = 8;       // warps per CTA
-constexpr int kApTokens = 16;     // tokens a warp holds in registers
+// A warp holds 16 tokens (bf16) or 8 (fp32) in registers, 32 bytes of registers
+// a lane and token pair either way; a team of page / tokens warps takes a page.
+template <typename E> struct ApGeom {
+    static constexpr int kTokens = sizeof(E) == 4 ? 8 : 16;
+    static constexpr int kWarps = sizeof(E) == 4 ? 16 : 8;  // per CTA: at least a team of the largest page
+};
 
 // A run of tokens that one page takes: the first token and how many.
 struct Run {
@@ -56,6 +62,28 @@ __device__ __forceinline__ Run next_run(const int32_t *row, int j, int end, int 
     return r;
 }
 
+// The run of a piece of a row whose slots follow one another from the row's
+// first slot on, as spark_pages_extend writes them: tokens [j, end) lie in one
+// page, and negative slots may follow.  False: they do not (any other map).
+__device__ __forceinline__ bool plain_run(const int32_t *row, int j, int end, int page, int n_slots, int place, Run &r) {
+    const int lane = threadIdx.x & 31;
+    r = {j, 0, 0};
+    bool plain = true, open = true;  // open: no slot has broken off yet
+#pragma unroll 1
+    for (int i0 = 0; i0 < end - j; i0 += 32) {
+        const int i = i0 + lane;
+        const int s = j + i < end ? row[j + i] : -1;
+        if (i0 == 0) r.slot = __shfl_sync(0xffffffffu, s, 0);
+        const uint32_t off = __ballot_sync(0xffffffffu, s < 0 || s != r.slot + i);
+        const uint32_t used = __ballot_sync(0xffffffffu, s >= 0);
+        const int k = open ? (off ? __ffs(off) - 1 : 32) : 0;
+        r.n += k;
+        open = open && off == 0;
+        plain = plain && (k == 32 || (used >> k) == 0);
+    }
+    return plain && (r.n == 0 || (r.slot < n_slots && (r.slot & (page - 1)) == place));
+}
+
 // Warps of one team meet (each team of a CTA has its own barrier).
 __device__ __forceinline__ void team_sync(int team, int warps) {
     if (warps == 1)
@@ -64,78 +92,163 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
 }
 
+// Largest |x| of the loaded values, infinities and NaN left out.  On the bits:
+// without the sign they order like the numbers, with infinities and NaN on top.
+template <typename E, int kLoads>
+__device__ __forceinline__ float largest(const uint4 (&x)[kLoads], bool *special) {
+    constexpr bool kWide = sizeof(E) == 4;
+    constexpr uint32_t kSign = kWide ? 0x7fffffffu : 0x7fff7fffu, kInf = kWide ? 0x7f800000u : 0x7f80u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = (&x[i].x)[j] & kSign;
+            m = kWide ? max(m, w) : __vmaxu2(m, w);
+        }
+    if (!kWide) m = max(m & 0xffffu, m >> 16);
+    m = __reduce_max_sync(0xffffffffu, m);
+    *special = m >= kInf;
+    if (*special) {  // once more, without them
+        m = 0;
+#pragma unroll 1
+        for (int i = 0; i < kLoads; ++i) {
+            uint4 v = x[0];
+#pragma unroll
+            for (int u = 1; u < kLoads; ++u)
+                if (u == i) v = x[u];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = (&v.x)[j] & kSign;
+                if (kWide) {
+                    m = w < kInf ? max(m, w) : m;
+                } else {
+                    if ((w & 0xffffu) < kInf) m = max(m, w & 0xffffu);
+                    if ((w >> 16) < kInf) m = max(m, w >> 16);
+                }
+            }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
+    return __uint_as_float(kWide ? m : m << 16);
+}
+
+template <typename E> __device__ __forceinline__ void unpack4(const uint4 &x, int half, float (&f)[4]) {
+    if (sizeof(E) == 4) {
+        f[0] = __uint_as_float(x.x);
+        f[1] = __uint_as_float(x.y);
+        f[2] = __uint_as_float(x.z);
+        f[3] = __uint_as_float(x.w);
+    } else {
+        const uint32_t a = half ? x.z : x.x, b = half ? x.w : x.y;
+        f[0] = __uint_as_float(a << 16);
+        f[1] = __uint_as_float(a & 0xffff0000u);
+        f[2] = __uint_as_float(b << 16);
+        f[3] = __uint_as_float(b & 0xffff0000u);
+    }
+}
+
+// Codes of four values.  int8 without special values: adding 1.5 * 2^23 rounds
+// to a whole number (to even at ties) and leaves it in the low byte.
+template <int kType> __device__ __forceinline__ uint32_t encode4(const float (&f)[4], float inv, bool special) {
+    if (kType == SPARK_KV8_I8 && !special) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(fmaf(f[i], inv, 12582912.f));
+        return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    }
+    const uint16_t lo = (uint16_t)kv8_encode2<kType>(f[0] * inv, f[1] * inv);
+    const uint16_t hi = (uint16_t)kv8_encode2<kType>(f[2] * inv, f[3] * inv);
+    uint32_t r;
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
+    return r;
+}
+
+// 4 CTAs of 8 warps (2 of 16) on an SM: the chain slots -> values -> codes is
+// hidden by 32 warps with 4 KB under way each, not inside one.
 template <typename E, int kType>
-__global__ void __launch_bounds__(kApWarps * 32)
+__global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps)
     kv8_append_kernel(const E *__restrict__ k_new, const E *__restrict__ v_new, int B, int n_cap,
-                      const int32_t *__restrict__ slots, spark_kv8cache kc, int pieces, uint32_t *status) {
-    __shared__ float part[kApWarps];
+                      const int32_t *__restrict__ slots, spark_kv8cache kc, int pieces, int per, uint32_t *status) {
+    constexpr int kWarps = ApGeom<E>::kWarps, kTokens = ApGeom<E>::kTokens;
+    __shared__ float part[kWarps];
     constexpr int kVec = 16 / (int)sizeof(E);       // values per 16-byte load
     constexpr int kRowLanes = kD / kVec;            // lanes per token: 16 (bf16) or 32 (fp32)
     constexpr int kPer = 32 / kRowLanes;            // tokens per load instruction
-    constexpr int kLoads = kApTokens / kPer;
+    constexpr int kLoads = kTokens / kPer;          // 8
     const int page = kc.page, Hkv = kc.Hkv;
-    const int tw = page / kApTokens;                // warps per team
+    const int tw = page / kTokens;                  // warps per team
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int team = warp / tw, wt = warp % tw;
-    const long units = (long)B * pieces * Hkv * 2;
-    const long unit = (long)blockIdx.x * (kApWarps / tw) + team;
-    if (unit >= units) return;
-    const bool is_v = (unit & 1) != 0;
-    const int h = (int)((unit >> 1) % Hkv);
-    const int piece = (int)((unit >> 1) / Hkv % pieces), b = (int)((unit >> 1) / Hkv / pieces);
+    const int team = warp / tw, wt = warp - team * tw;
+    // a team's work: `per` of the 2 * Hkv (head, key or value)s of one piece of one row
+    const unsigned shares = (unsigned)(2 * Hkv + per - 1) / (unsigned)per;
+    const unsigned unit = blockIdx.x * (unsigned)(kWarps / tw) + (unsigned)team;
+    const unsigned bp = unit / shares, b = bp / (unsigned)pieces;
+    if (b >= (unsigned)B) return;
+    const int piece = (int)(bp - b * (unsigned)pieces), first = (int)(unit - bp * shares) * per;
+    const int last = min(first + per, 2 * Hkv);
     const int32_t *row = slots + (size_t)b * n_cap;
-    const E *src = (is_v ? v_new : k_new) + ((size_t)b * Hkv + h) * n_cap * kD;
-    uint8_t *codes = static_cast<uint8_t *>(is_v ? kc.v : kc.k);
-    float *scales = is_v ? kc.v_scale : kc.k_scale;
-    const int end = min(n_cap, (piece + 1) * page), n_slots = kc.n_pages * page;
+    const int n_slots = kc.n_pages * page;
+    // a piece is what falls into one page if the row's slots follow one another
+    const int o0 = max(row[0], 0) & (page - 1);
+    const int begin = max(0, piece * page - o0), end = min(n_cap, (piece + 1) * page - o0);
+    if (begin >= end) return;
     bool bad = false;
-    Run r = next_run(row, piece * page, end, n_cap, page, n_slots, &bad);
+    Run run;
+    const bool plain = plain_run(row, begin, end, page, n_slots, (begin + o0) & (page - 1), run);
+    if (!plain) run = next_run(row, begin, end, n_cap, page, n_slots, &bad);
+    if (run.n == 0) {
+        if (bad) atomicOr(status, kDevBadArg);
+        return;
+    }
+#pragma unroll 1
+    for (int w = first; w < last; ++w) {
+    const int h = w >> 1;
+    const E *src = ((w & 1) ? v_new : k_new) + ((size_t)b * Hkv + h) * n_cap * kD;
+    uint8_t *codes = static_cast<uint8_t *>((w & 1) ? kc.v : kc.k);
+    float *scales = (w & 1) ? kc.v_scale : kc.k_scale;
+    Run r = run;
+#pragma unroll 1
     while (r.n > 0) {
         const int o = r.slot & (page - 1);
         const size_t ph = (size_t)(r.slot / page) * Hkv + h;
         uint8_t *dst = codes + ph * page * kD;
-        // this warp's tokens of the run: t0 .. t0 + 15
-        const int t0 = wt * kApTokens, sub = lane / kRowLanes, col = lane % kRowLanes;
+        // this warp's tokens of the run: t0 ..
+        const int t0 = wt * kTokens, sub = lane / kRowLanes, col = lane % kRowLanes;
         uint4 x[kLoads];
         const float old = o > 0 ? scales[ph] : 0.f;
-        float a = 0.f;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int t = t0 + i * kPer + sub;
-            x[i] = t < r.n ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t) * kD) + col)
+            x[i] = t < r.n ? __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t) * kD) + col)
                            : make_uint4(0, 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const E *e = reinterpret_cast<const E *>(&x[i]);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float y = fabsf(Elem<E>::to_f(e[j]));
-                a = y < INFINITY ? fmaxf(a, y) : a;  // infinities and NaN do not set the scale
-            }
-        }
-        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+        bool special;
+        float a = largest<E, kLoads>(x, &special);
         if (tw > 1) {
             team_sync(team, tw);  // the last run's maxima have been read
             if (lane == 0) part[warp] = a;
             team_sync(team, tw);
-            for (int i = 0; i < tw; ++i) a = fmaxf(a, part[team * tw + i]);
+            a = lane < tw ? part[team * tw + lane] : 0.f;
+            a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
         }
         const int ex = kv8_exponent<kType>(a);
         const float need = exp2_int(ex);
+        special |= ex == kKv8MaxExp;  // values may lie beyond the largest code
         const bool keeps = o > 0 && old >= need;
         const float inv = keeps ? 1.0f / old : exp2_int(-ex);
         if (o > 0 && !keeps) {  // the page's codes move to the larger scale
             const float ratio = old * inv;
+#pragma unroll 1
             for (int i = wt * 32 + lane; i < o * (kD / 16); i += tw * 32) {
                 uint4 w = *(reinterpret_cast<const uint4 *>(dst) + i);
-                uint32_t *u = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 lo = __half22float2(kv8_decode2<kType>(u[j] & 0xffffu));
-                    const float2 hi = __half22float2(kv8_decode2<kType>(u[j] >> 16));
-                    u[j] = kv8_encode2<kType>(lo.x * ratio, lo.y * ratio) |
-                           (kv8_encode2<kType>(hi.x * ratio, hi.y * ratio) << 16);
+                    uint32_t &c = (&w.x)[j];
+                    const float2 lo = __half22float2(kv8_decode2<kType>(c & 0xffffu));
+                    const float2 hi = __half22float2(kv8_decode2<kType>(c >> 16));
+                    c = kv8_encode2<kType>(lo.x * ratio, lo.y * ratio) |
+                        (kv8_encode2<kType>(hi.x * ratio, hi.y * ratio) << 16);
                 }
                 *(reinterpret_cast<uint4 *>(dst) + i) = w;
             }
@@ -145,12 +258,13 @@ __global__ void __launch_bounds__(kApWarps * 32)
         for (int i = 0; i < kLoads; ++i) {
             const int t = t0 + i * kPer + sub;
             if (t < r.n) {
-                const E *e = reinterpret_cast<const E *>(&x[i]);
                 uint32_t c[kVec / 4];
 #pragma unroll
-                for (int j = 0; j < kVec; j += 4)
-                    c[j / 4] = kv8_encode2<kType>(Elem<E>::to_f(e[j]) * inv, Elem<E>::to_f(e[j + 1]) * inv) |
-                               (kv8_encode2<kType>(Elem<E>::to_f(e[j + 2]) * inv, Elem<E>::to_f(e[j + 3]) * inv) << 16);
+                for (int j = 0; j < kVec / 4; ++j) {
+                    float f[4];
+                    unpack4<E>(x[i], j, f);
+                    c[j] = encode4<kType>(f, inv, special);
+                }
                 uint8_t *to = dst + (size_t)(o + t) * kD + col * kVec;
                 if (kVec == 8)
                     *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[kVec / 4 - 1]);
@@ -158,38 +272,45 @@ __global__ void __launch_bounds__(kApWarps * 32)
                     *reinterpret_cast<uint32_t *>(to) = c[0];
             }
         }
+        if (plain) break;
         // a later run of this piece may lie in the same page
         __threadfence_block();
         team_sync(team, tw);
         r = next_run(row, r.j + r.n, end, n_cap, page, n_slots, &bad);
+    }
     }
     if (bad) atomicOr(status, kDevBadArg);
 }
 
 template <typename E>
 static cudaError_t launch_append(const E *k_new, const E *v_new, int B, int n_cap, const int32_t *slots,
-                                 const spark_kv8cache &kc, void *ws, cudaStream_t st) {
-    const int pieces = (n_cap + kc.page - 1) / kc.page;
-    const int teams = kApWarps / (kc.page / kApTokens);
-    const long units = (long)B * pieces * kc.Hkv * 2;
+                                 const spark_kv8cache &kc, void *ws, int num_sms, cudaStream_t st) {
+    constexpr int kWarps = ApGeom<E>::kWarps;
+    const int pieces = (n_cap + kc.page - 2) / kc.page + 1;  // a row may start on a page's last place
+    const int teams = kWarps / (kc.page / ApGeom<E>::kTokens);
+    // With plenty of work a team takes several heads, which share its look at the
+    // slots; three rounds of resident teams are left so that the last one evens out.
+    const long all = (long)B * pieces * kc.Hkv * 2;
+    const int per = (int)std::min<long>(std::max<long>(all * (kWarps / teams) / (3l * num_sms * 32), 1), 2 * kc.Hkv);
+    const long units = (long)B * pieces * ((2 * kc.Hkv + per - 1) / per);
     const unsigned grid = (unsigned)((units + teams - 1) / teams);
     uint32_t *status = static_cast<uint32_t *>(ws);
     if (kc.type == SPARK_KV8_E4M3)
-        kv8_append_kernel<E, SPARK_KV8_E4M3><<<grid, kApWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc,
-                                                                             pieces, status);
+        kv8_append_kernel<E, SPARK_KV8_E4M3><<<grid, kWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc, pieces,
+                                                                           per, status);
     else
-        kv8_append_kernel<E, SPARK_KV8_I8><<<grid, kApWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc,
-                                                                           pieces, status);
+        kv8_append_kernel<E, SPARK_KV8_I8><<<grid, kWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc, pieces, per,
+                                                                         status);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype,
-                              const int32_t *slots, const spark_kv8cache &kc, void *ws, cudaStream_t st) {
+                              const int32_t *slots, const spark_kv8cache &kc, void *ws, int num_sms, cudaStream_t st) {
     if (dtype == SPARK_F32)
         return launch_append(static_cast<const float *>(k_new), static_cast<const float *>(v_new), B, n_cap, slots, kc,
-                             ws, st);
+                             ws, num_sms, st);
     return launch_append(static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new), B,
-                         n_cap, slots, kc, ws, st);
+                         n_cap, slots, kc, ws, num_sms, st);
 }
 
 }  // namespace spark
