@@ -398,9 +398,10 @@ def spark_tail_append(k_new, v_new, k_tail, v_tail, B, Hkv, D, tail_cap, slot, s
 
 
 # ------------------------------------------------------ paged 8-bit cache
-@dataclass
+@dataclass(frozen=True)
 class KV8Cache:
-    """Device tensors of the paged 8-bit cache (layout of include/spark.h)."""
+    """Device tensors of the paged 8-bit cache (layout of include/spark.h).
+    Frozen: the descriptor that the calls pass is made once, here."""
     n_pages: int
     Hkv: int
     page: int             # tokens per page: 16, 32, 64 or 128
@@ -417,8 +418,11 @@ class KV8Cache:
                                    ("k_scale", self.k_scale, scales, torch.float32),
                                    ("v_scale", self.v_scale, scales, torch.float32)):
             _need(t, name, dt, shape, self.k.device)
-        self._struct = spark_kv8cache(self.n_pages, self.Hkv, self.page, self.D, self.type, _ptr(self.k),
-                                      _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale))
+        desc = spark_kv8cache(self.n_pages, self.Hkv, self.page, self.D, self.type, _ptr(self.k), _ptr(self.v),
+                              _ptr(self.k_scale), _ptr(self.v_scale))
+        object.__setattr__(self, "_struct", desc)
+        object.__setattr__(self, "ref", ctypes.byref(desc))
+        object.__setattr__(self, "index", self.k.get_device())
 
     @staticmethod
     def empty(n_pages, Hkv, page, type=SPARK_KV8_E4M3, D=128, device="cuda") -> "KV8Cache":
@@ -446,10 +450,19 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
         raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {device}")
 
 
-def _launch_stream(device, stream) -> int | None:
-    """The stream to launch on; kernels start on the current device, so the tensors must be there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}: they must be on the current CUDA device")
+def _fits(t: torch.Tensor, dtype, shape, index: int) -> bool:
+    """_need's checks in the few hundred nanoseconds that a decode step's calls
+    can spare for each tensor; on False, _need says what is wrong."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
+
+
+def _launch_stream(index: int, stream) -> int | None:
+    """The stream to launch on; kernels start on the current device, so the
+    tensors (on device `index`) must be there."""
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
@@ -464,17 +477,23 @@ def spark_pages_extend(lens: torch.Tensor, n_new: torch.Tensor, page: int, pool:
                        ws: torch.Tensor, stream=None) -> None:
     """Pages for each row's n_new tokens (table [B, cap] and taken_out) and
     their slots [B, n_cap]; lens_out / taken_out may be lens / taken."""
-    B, dev, i32 = lens.shape[0], lens.device, torch.int32
-    cap, n_cap, n_pages = table.shape[-1], slots.shape[-1], pool.shape[0]
-    for t, name, shape in ((lens, "lens", (B,)), (n_new, "n_new", (B,)), (pool, "pool", (n_pages,)),
-                           (taken, "taken", (1,)), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
-                           (lens_out, "lens_out", (B,)), (taken_out, "taken_out", (1,))):
-        _need(t, name, i32, shape, dev)
+    i32, index = torch.int32, lens.get_device()
+    B, cap, n_cap, n_pages = lens.shape[0], table.shape[-1], slots.shape[-1], pool.shape[0]
+    row, one = (B,), (1,)
+    if not (_fits(lens, i32, row, index) and _fits(n_new, i32, row, index) and _fits(pool, i32, (n_pages,), index)
+            and _fits(taken, i32, one, index) and _fits(table, i32, (B, cap), index)
+            and _fits(slots, i32, (B, n_cap), index) and _fits(lens_out, i32, row, index)
+            and _fits(taken_out, i32, one, index)):
+        for t, name, shape in ((lens, "lens", row), (n_new, "n_new", row), (pool, "pool", (n_pages,)),
+                               (taken, "taken", one), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
+                               (lens_out, "lens_out", row), (taken_out, "taken_out", one)):
+            _need(t, name, i32, shape, lens.device)
     rc = lib().spark_pages_extend(lens.data_ptr(), n_new.data_ptr(), B, page, pool.data_ptr(), n_pages,
                                   taken.data_ptr(), table.data_ptr(), cap, n_cap, slots.data_ptr(),
-                                  lens_out.data_ptr(), taken_out.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _launch_stream(dev, stream))
-    _check(rc, "spark_pages_extend")
+                                  lens_out.data_ptr(), taken_out.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                  _launch_stream(index, stream))
+    if rc:
+        _check(rc, "spark_pages_extend")
 
 
 def spark_pages_trim(lens: torch.Tensor, keep: torch.Tensor, page: int, pool: torch.Tensor, taken: torch.Tensor,
@@ -482,16 +501,21 @@ def spark_pages_trim(lens: torch.Tensor, keep: torch.Tensor, page: int, pool: to
                      stream=None) -> None:
     """Cut each row to its first keep tokens and give the pages behind them
     back to the pool; lens_out / taken_out may be lens / taken."""
-    B, dev, i32 = lens.shape[0], lens.device, torch.int32
-    cap, n_pages = table.shape[-1], pool.shape[0]
-    for t, name, shape in ((lens, "lens", (B,)), (keep, "keep", (B,)), (pool, "pool", (n_pages,)),
-                           (taken, "taken", (1,)), (table, "table", (B, cap)), (lens_out, "lens_out", (B,)),
-                           (taken_out, "taken_out", (1,))):
-        _need(t, name, i32, shape, dev)
+    i32, index = torch.int32, lens.get_device()
+    B, cap, n_pages = lens.shape[0], table.shape[-1], pool.shape[0]
+    row, one = (B,), (1,)
+    if not (_fits(lens, i32, row, index) and _fits(keep, i32, row, index) and _fits(pool, i32, (n_pages,), index)
+            and _fits(taken, i32, one, index) and _fits(table, i32, (B, cap), index)
+            and _fits(lens_out, i32, row, index) and _fits(taken_out, i32, one, index)):
+        for t, name, shape in ((lens, "lens", row), (keep, "keep", row), (pool, "pool", (n_pages,)),
+                               (taken, "taken", one), (table, "table", (B, cap)), (lens_out, "lens_out", row),
+                               (taken_out, "taken_out", one)):
+            _need(t, name, i32, shape, lens.device)
     rc = lib().spark_pages_trim(lens.data_ptr(), keep.data_ptr(), B, page, pool.data_ptr(), n_pages,
                                 taken.data_ptr(), table.data_ptr(), cap, lens_out.data_ptr(), taken_out.data_ptr(),
-                                ws.data_ptr(), ws.numel() * ws.element_size(), _launch_stream(dev, stream))
-    _check(rc, "spark_pages_trim")
+                                ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    if rc:
+        _check(rc, "spark_pages_trim")
 
 
 def spark_kv8_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, kc: KV8Cache, ws: torch.Tensor,
@@ -499,15 +523,17 @@ def spark_kv8_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tens
     """Write k_new, v_new [B, Hkv, n_cap, D] into the slots [B, n_cap] in 8
     bits ([B, Hkv, D] with n_cap = 1)."""
     B, n_cap = slots.shape
-    dev = kc.k.device
-    shape = (B, kc.Hkv, kc.D) if k_new.dim() == 3 and n_cap == 1 else (B, kc.Hkv, n_cap, kc.D)
-    _need(k_new, "k_new", k_new.dtype, shape, dev)
-    _need(v_new, "v_new", k_new.dtype, shape, dev)
-    _need(slots, "slots", torch.int32, (B, n_cap), dev)
-    rc = lib().spark_kv8_append(k_new.data_ptr(), v_new.data_ptr(), B, n_cap, _dtype_code(k_new.dtype),
-                                slots.data_ptr(), ctypes.byref(kc.struct()), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _launch_stream(dev, stream))
-    _check(rc, "spark_kv8_append")
+    index, dt = kc.index, k_new.dtype
+    shape = (B, kc.Hkv, kc.D) if n_cap == 1 and k_new.dim() == 3 else (B, kc.Hkv, n_cap, kc.D)
+    if not (_fits(k_new, dt, shape, index) and _fits(v_new, dt, shape, index)
+            and _fits(slots, torch.int32, (B, n_cap), index)):
+        _need(k_new, "k_new", dt, shape, kc.k.device)
+        _need(v_new, "v_new", dt, shape, kc.k.device)
+        _need(slots, "slots", torch.int32, (B, n_cap), kc.k.device)
+    rc = lib().spark_kv8_append(k_new.data_ptr(), v_new.data_ptr(), B, n_cap, _dtype_code(dt), slots.data_ptr(),
+                                kc.ref, ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    if rc:
+        _check(rc, "spark_kv8_append")
 
 
 def spark_decode_attn_kv8(q: torch.Tensor, kc: KV8Cache, table: torch.Tensor, lens: torch.Tensor, G: int,
@@ -515,19 +541,28 @@ def spark_decode_attn_kv8(q: torch.Tensor, kc: KV8Cache, table: torch.Tensor, le
     """Attention of q [B, Hkv*G, n_q, D] (or [B, Hkv*G, D]), each row's newest
     tokens, over its pages; out fp32, shaped like q."""
     B, cap = table.shape
-    dev = kc.k.device
-    n_q = q.shape[2] if q.dim() == 4 else 1
-    shape = (B, kc.Hkv * G, n_q, kc.D) if q.dim() == 4 else (B, kc.Hkv * G, kc.D)
-    _need(q, "q", q.dtype, shape, dev)
-    _need(out, "out", torch.float32, shape, dev)
-    _need(table, "table", torch.int32, (B, cap), dev)
-    _need(lens, "lens", torch.int32, (B,), dev)
-    if n_new is not None:
-        _need(n_new, "n_new", torch.int32, (B,), dev)
-    rc = lib().spark_decode_attn_kv8(q.data_ptr(), _dtype_code(q.dtype), ctypes.byref(kc.struct()),
-                                     table.data_ptr(), cap, lens.data_ptr(), _ptr(n_new), B, G, n_q, out.data_ptr(),
-                                     ws.data_ptr(), ws.numel() * ws.element_size(), _launch_stream(dev, stream))
-    _check(rc, "spark_decode_attn_kv8")
+    index, i32, dt = kc.index, torch.int32, q.dtype
+    if q.dim() == 4:
+        n_q = q.shape[2]
+        shape = (B, kc.Hkv * G, n_q, kc.D)
+    else:
+        n_q, shape = 1, (B, kc.Hkv * G, kc.D)
+    row = (B,)
+    if not (_fits(q, dt, shape, index) and _fits(out, torch.float32, shape, index)
+            and _fits(table, i32, (B, cap), index) and _fits(lens, i32, row, index)
+            and (n_new is None or _fits(n_new, i32, row, index))):
+        dev = kc.k.device
+        _need(q, "q", dt, shape, dev)
+        _need(out, "out", torch.float32, shape, dev)
+        _need(table, "table", i32, (B, cap), dev)
+        _need(lens, "lens", i32, row, dev)
+        if n_new is not None:
+            _need(n_new, "n_new", i32, row, dev)
+    rc = lib().spark_decode_attn_kv8(q.data_ptr(), _dtype_code(dt), kc.ref, table.data_ptr(), cap, lens.data_ptr(),
+                                     None if n_new is None else n_new.data_ptr(), B, G, n_q, out.data_ptr(),
+                                     ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    if rc:
+        _check(rc, "spark_decode_attn_kv8")
 
 
 def spark_workspace_bytes_kv8(B: int, Hkv: int, G: int, n_q: int = 1) -> int:

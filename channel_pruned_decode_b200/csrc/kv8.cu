@@ -9,8 +9,6 @@
 // value is read once and its code written once.
 #include "kv8.cuh"
 
-#include <algorithm>
-
 namespace spark {
 
 // A warp holds 16 tokens (bf16) or 8 (fp32) in registers, 32 bytes of registers
@@ -215,13 +213,17 @@ __global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps
         uint8_t *dst = codes + ph * page * kD;
         // this warp's tokens of the run: t0 ..
         const int t0 = wt * kTokens, sub = lane / kRowLanes, col = lane % kRowLanes;
+        const bool whole = t0 + kTokens <= r.n;  // all of this warp's tokens are there
         uint4 x[kLoads];
         const float old = o > 0 ? scales[ph] : 0.f;
+        const uint4 *from = reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t0 + sub) * kD) + col;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int t = t0 + i * kPer + sub;
-            x[i] = t < r.n ? __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t) * kD) + col)
-                           : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kLoads; ++i) x[i] = __ldcs(from + i * kPer * (kD / kVec));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                x[i] = t0 + i * kPer + sub < r.n ? __ldcs(from + i * kPer * (kD / kVec)) : make_uint4(0, 0, 0, 0);
         }
         bool special;
         float a = largest<E, kLoads>(x, &special);
@@ -254,22 +256,21 @@ __global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps
             }
         }
         if (wt == 0 && lane == 0 && !keeps) scales[ph] = need;
+        uint8_t *to = dst + (size_t)(o + t0 + sub) * kD + col * kVec;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int t = t0 + i * kPer + sub;
-            if (t < r.n) {
-                uint32_t c[kVec / 4];
+            uint32_t c[kVec / 4];
 #pragma unroll
-                for (int j = 0; j < kVec / 4; ++j) {
-                    float f[4];
-                    unpack4<E>(x[i], j, f);
-                    c[j] = encode4<kType>(f, inv, special);
-                }
-                uint8_t *to = dst + (size_t)(o + t) * kD + col * kVec;
+            for (int j = 0; j < kVec / 4; ++j) {
+                float f[4];
+                unpack4<E>(x[i], j, f);
+                c[j] = encode4<kType>(f, inv, special);
+            }
+            if (whole || t0 + i * kPer + sub < r.n) {
                 if (kVec == 8)
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[kVec / 4 - 1]);
+                    *reinterpret_cast<uint2 *>(to + i * kPer * kD) = make_uint2(c[0], c[kVec / 4 - 1]);
                 else
-                    *reinterpret_cast<uint32_t *>(to) = c[0];
+                    *reinterpret_cast<uint32_t *>(to + i * kPer * kD) = c[0];
             }
         }
         if (plain) break;
@@ -288,10 +289,12 @@ static cudaError_t launch_append(const E *k_new, const E *v_new, int B, int n_ca
     constexpr int kWarps = ApGeom<E>::kWarps;
     const int pieces = (n_cap + kc.page - 2) / kc.page + 1;  // a row may start on a page's last place
     const int teams = kWarps / (kc.page / ApGeom<E>::kTokens);
-    // With plenty of work a team takes several heads, which share its look at the
-    // slots; three rounds of resident teams are left so that the last one evens out.
-    const long all = (long)B * pieces * kc.Hkv * 2;
-    const int per = (int)std::min<long>(std::max<long>(all * (kWarps / teams) / (3l * num_sms * 32), 1), 2 * kc.Hkv);
+    // Where the GPU is full more than once, a team takes the keys and the values
+    // of a head, which share its look at the slots.  32 x 2048 tokens of 8 heads
+    // in bf16: 1 at a time 77.7 us, 2 70.1, 4 71.4, 8 75.4, 16 77.0; 5 x 1777
+    // tokens of 4 heads in fp32: 14.4, 13.6, 16.1, 24.6 (the GPU no longer full).
+    const long warps = (long)B * pieces * kc.Hkv * 2 * (kWarps / teams);
+    const int per = warps > 32l * num_sms ? 2 : 1;
     const long units = (long)B * pieces * ((2 * kc.Hkv + per - 1) / per);
     const unsigned grid = (unsigned)((units + teams - 1) / teams);
     uint32_t *status = static_cast<uint32_t *>(ws);
