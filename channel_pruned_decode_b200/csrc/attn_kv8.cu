@@ -310,11 +310,22 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         mbar_init(smem_u32(&empty[tid]), tw);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // what needs no memory, before the wait
+    int qi[kN][2];  // which of its head's queries rows 2c, 2c + 1 of each group are (n_q: none)
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = wt * kRows + (kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3);
+            qi[t][j] = row < a.rows ? row % a.n_q : a.n_q;
+        }
+    const int parts = max(1, kAtWarps / a.rows);  // of the last merge: warps per row
+    const int mg_row = warp / parts, mg_part = warp - mg_row * parts;
+    const int per = (a.B + kAtThreads - 1) / kAtThreads, n_look = (a.B + per - 1) / max(per, 1);  // rows a thread looks at
     let_next_kernel_start();
     wait_for_prior_kernel();
 
     // ---- the line: steps before each thread's rows, and in all
-    const int per = (a.B + kAtThreads - 1) / kAtThreads;
     {
         int mine = 0;
         bool bad = false;
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         --to_issue;
     };
     if (wt == 0 && steps > 0) {  // the step where the team starts
-        int lo = 0, hi = kAtThreads;  // the last thread whose rows start at or before it
+        int lo = 0, hi = n_look;  // the last thread whose rows start at or before it
 #pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -441,14 +452,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     float qf[kN][2];              // score factor of rows 2c, 2c + 1
     int lim[kN][2];               // the last token they see
     float o[kN][8][4], m[kN][2], l[kN][2];
-    int qi[kN][2];                // which of its head's queries they are (n_q: none)
-#pragma unroll
-    for (int t = 0; t < kN; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = wt * kRows + (kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3);
-            qi[t][j] = row < a.rows ? row % a.n_q : a.n_q;
-        }
     float E_top = 1.f, E_inv = 1.f;
     int b = -1, h = 0, nn = 0, first_full = 0;
     bool starts_pair = false, ends_pair = false;
@@ -831,6 +834,15 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) cross[i] = job[i] && (x0[i] < cta_from || x1[i] >= cta_to);
     }
+    int c0x[2] = {0, 0}, c1x[2] = {0, 0};  // CTAs that share the pair
+    if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (cross[i]) {
+                c0x[i] = x0[i] / cta_share;
+                c1x[i] = x1[i] / cta_share;
+            }
+    }
     int turn = 0;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
@@ -892,21 +904,19 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!cross[i]) continue;
-            const int c0 = x0[i] / cta_share, c1 = x1[i] / cta_share;
-            const uint32_t seen = add_acq_rel(a.counter + c0);
-            if (seen == (uint32_t)(c1 - c0)) {
-                a.counter[c0] = 0;  // as the next call needs it
-                const int k = c0 < (int)blockIdx.x ? 0 : 1;  // the CTA's first pair, or its last
-                last_c0[k] = c0;
-                last_c1[k] = c1;
+            const uint32_t seen = add_acq_rel(a.counter + c0x[i]);
+            if (seen == (uint32_t)(c1x[i] - c0x[i])) {
+                a.counter[c0x[i]] = 0;  // as the next call needs it
+                const int k = c0x[i] < (int)blockIdx.x ? 0 : 1;  // the CTA's first pair, or its last
+                last_c0[k] = c0x[i];
+                last_c1[k] = c1x[i];
                 last_nn[k] = qn[i];
                 last_pair[k] = pr[i];
             }
         }
     }
     __syncthreads();
-    const int parts = max(1, kAtWarps / a.rows);  // warps per row
-    float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + 64 * kD;  // at most 64 (row, part)s
+    float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + kAtWarps * kD;  // one (row, part) a warp where a row has several
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const int pair = uniform(last_pair[k]);
@@ -914,8 +924,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         const int c0 = uniform(last_c0[k]), n = uniform(last_c1[k]) - c0 + 1, each = (n + parts - 1) / parts;
         const int nn_p = uniform(last_nn[k]);
 #pragma unroll 1
-        for (int it = warp; it < a.rows * parts; it += kAtWarps) {
-            const int row = it / parts, i0 = (it - row * parts) * each, i1 = min(n, i0 + each);
+        for (int row = mg_row; row < a.rows; row += kAtWarps) {
+            const int i0 = mg_part * each, i1 = min(n, i0 + each);
             if (a.n_q > 1 && row % a.n_q >= nn_p) continue;
             Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
@@ -941,8 +951,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (parts == 1) {
                 write_row(a.out + ((size_t)pair * a.rows + row) * kD, r);
             } else {
-                reinterpret_cast<float4 *>(sm_acc + it * kD)[lane] = r.acc;
-                if (lane == 0) reinterpret_cast<float2 *>(sm_ml)[it] = make_float2(r.m, r.l);
+                reinterpret_cast<float4 *>(sm_acc + warp * kD)[lane] = r.acc;
+                if (lane == 0) reinterpret_cast<float2 *>(sm_ml)[warp] = make_float2(r.m, r.l);
             }
         }
         if (parts == 1) continue;
