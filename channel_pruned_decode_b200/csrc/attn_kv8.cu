@@ -750,9 +750,14 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             for (int i = 0; i < 4; ++i) {
                 const int row = hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
                 w[i] = lds128(vb + (uint32_t)row * kD + ((uint32_t)(g ^ (row & 7)) << 4));
-                if (kType == SPARK_KV8_E4M3 && hide && t0 + row >= first_full)
-                    w[i] = make_uint4(w[i].x & ~nan_codes(w[i].x), w[i].y & ~nan_codes(w[i].y),
-                                      w[i].z & ~nan_codes(w[i].z), w[i].w & ~nan_codes(w[i].w));
+            }
+            if (kType == SPARK_KV8_E4M3 && hide) {
+                __syncwarp();  // a branch, not predicates on the common path
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t0 + hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8 >= first_full)
+                        w[i] = make_uint4(w[i].x & ~nan_codes(w[i].x), w[i].y & ~nan_codes(w[i].y),
+                                          w[i].z & ~nan_codes(w[i].z), w[i].w & ~nan_codes(w[i].w));
             }
             const uint32_t ww[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
                                        {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
