@@ -44,6 +44,7 @@ constexpr int kMaxStages = 24;             // stages of a CTA: 192 KB
 constexpr int kRingBytes = kMaxStages * kStageBytes;
 constexpr int kMinCtaSteps = 4;            // a CTA takes at least this many steps
 constexpr int kPScale = 6;                 // probabilities enter the second product times 2^6
+constexpr int kFlushSteps = 32;            // steps between two flushes of the running sums
 constexpr float kSlack = 8.f;              // log2 of how far a probability may pass its reference
 
 // What a stage's consumers need to know beside the codes.
@@ -509,9 +510,17 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
         }
     };
-    auto end_pair = [&](bool last) {
+    // The running sums leave the registers: at the end of a pair, and every
+    // kFlushSteps steps on the way.  The tensor cores cut off what they add up
+    // (towards zero), which over 110 steps grew to 4e-6 of the result and would
+    // go on growing; a flush puts what has come together into the team's partial
+    // in global memory and starts the sums at zero, and the next one adds it to
+    // theirs in fp32.
+    bool flushed = false;
+    auto put_sums = [&](bool last, bool on_the_way) {
         const long bh = (long)b * Hkv + h;
-        const bool whole = starts_pair && ends_pair;
+        const bool whole = starts_pair && ends_pair && !on_the_way;
+        last = last && !on_the_way;
         // A partial of the stretch's last pair goes to the team's own part of
         // the ring, which it has read by now; one of its first pair, with others
         // behind it, to global memory.
@@ -524,13 +533,31 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 s += __shfl_xor_sync(0xffffffffu, s, 4);
                 s += __shfl_xor_sync(0xffffffffu, s, 8);
                 s += __shfl_xor_sync(0xffffffffu, s, 16);
-                l[t][j] = s;
+                if (!on_the_way) l[t][j] = s;  // (a lane's own tokens until then)
             }
             if (kNT == 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[t][j][i] += __shfl_xor_sync(0xffffffffu, o[t][j][i], 2);
+            }
+            if (flushed) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (qi[t][j] >= nn) continue;
+                    const int row = wt * kRows + (kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3);
+                    const size_t at = (size_t)(tm + bh) * a.rows + row;
+                    const float was = __ldcg(a.ml + at * 2), keep = was == -INFINITY ? 0.f : exp2_approx(was - m[t][j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.acc + at * kD + g * 16) + i);
+                        o[t][2 * i][j] += v.x * keep * E_inv;
+                        o[t][2 * i][2 + j] += v.y * keep * E_inv;
+                        o[t][2 * i + 1][j] += v.z * keep * E_inv;
+                        o[t][2 * i + 1][2 + j] += v.w * keep * E_inv;
+                    }
+                }
+                __syncwarp();  // every lane has read the old partial
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -554,7 +581,12 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                         make_float4(o[t][2 * i][j] * f, o[t][2 * i][2 + j] * f, o[t][2 * i + 1][j] * f,
                                     o[t][2 * i + 1][2 + j] * f);
             }
+            if (on_the_way) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+            }
         }
+        flushed = on_the_way;
     };
 
     // One loop fills the ring (it < 0), consumes the steps, and ends the last
@@ -563,6 +595,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     int st = 0, put = 0;  // stages: next to consume, next to fill
     uint32_t parity = 0;
     bool failed = false;
+    int since = 0;  // steps whose sums are in the registers
 #pragma unroll 1
     for (int it = steps > 0 ? -ns : 1; it <= steps; ++it) {
         if (it >= 0) {
@@ -573,10 +606,14 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (!failed) failed = !wait_warp(smem_u32(&full[st0 + st]), parity);
             mt = meta[st0 + st];
         }
-        if (it == steps || (!failed && uniform(mt.b != b || mt.h != h))) {
+        const bool over = it == steps || (!failed && uniform(mt.b != b || mt.h != h));
+        if (over || since == kFlushSteps) {
+            since = 0;
             if (it == steps && opaque(tw) > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tw * 32) : "memory");
-            if (uniform(b >= 0) && !failed) end_pair(it == steps);
+            if (uniform(b >= 0) && !failed) put_sums(it == steps, !over);
             if (it == steps) break;
+        }
+        if (over) {
             begin_pair(mt);
             if (wt == 0 && lane == 0) {  // for the merge
                 const int i = it == 0 ? 0 : 1;
@@ -586,6 +623,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 stretch[team].nn[i] = stretch[team].nn[1] = nn;
             }
         }
+        ++since;
         ends_pair = mt.s + 1 == mt.n_steps;
         const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
         const int t0 = uniform(mt.s) * kStep;
