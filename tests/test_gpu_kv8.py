@@ -266,6 +266,61 @@ def test_attn_very_long():
     _check_attn([131072, 65537], 2, 4, 1, 32, SPARK_KV8_E4M3, torch.bfloat16)
 
 
+@pytest.mark.parametrize("G,n_q,kind", [(2, 1, SPARK_KV8_I8), (8, 1, SPARK_KV8_E4M3), (8, 2, SPARK_KV8_I8),
+                                        (16, 2, SPARK_KV8_E4M3)])
+def test_attn_long_stretches(G, n_q, kind):
+    """More steps to a warp than its running sums stay in registers for."""
+    _check_attn([150000, 150001, 7], 8, G, n_q, 128, kind, torch.bfloat16)
+
+
+def test_attn_many_rows():
+    """More rows than a CTA has threads; most of them without tokens."""
+    lens = [0] * 3000
+    for i, x in ((0, 5), (1, 40), (700, 129), (2047, 1), (2999, 333)):
+        lens[i] = x
+    _check_attn(lens, 1, 4, 1, 16, SPARK_KV8_E4M3, torch.float32)
+
+
+@pytest.mark.parametrize("lens", [[0, 0], [5, 0]])
+def test_attn_without_any_page(lens):
+    """A pool without pages, tables without places: nothing is seen, and rows that claim tokens are flagged."""
+    kc = KV8Cache.empty(0, 2, 16)
+    q = _values(_gen(5), (2, 8, 1, D))
+    out, ws = _attend(q, kc, torch.zeros((2, 0), dtype=torch.int32, device=DEV), lens, 4)
+    assert float(out.abs().max()) == 0.0
+    assert spark_device_status(ws) == (SPARK_ERR_ARG if any(lens) else 0)
+    out, ws = _attend(q, kc, torch.zeros((2, 3), dtype=torch.int32, device=DEV), lens, 4)
+    assert float(out.abs().max()) == 0.0
+    assert spark_device_status(ws) == (SPARK_ERR_ARG if any(lens) else 0)
+
+
+def test_attn_rows_that_share_pages():
+    """Rows may list the same pages (a common prefix), each with an end of its own."""
+    kc, table = _context([200, 200], 2, 16, SPARK_KV8_I8, 4)
+    table[1, :6] = table[0, :6]
+    lens = [200, 130]
+    q = _values(_gen(5), (2, 8, 1, D), torch.bfloat16)
+    out, ws = _attend(q, kc, table, lens, 4)
+    ref, tol = R.attention(q, kc.k, kc.v, kc.k_scale, kc.v_scale, SPARK_KV8_I8, table, lens, [1, 1], 4, 16)
+    assert bool(((out - ref).abs() <= tol).all())
+
+
+def test_attn_workspace_serves_calls_of_other_shapes():
+    """One workspace, sized for the largest call, through calls of different shapes in any order."""
+    shapes = [([3000, 10], 8, 4, 1), ([77] * 30, 2, 8, 2), ([20000], 1, 16, 4), ([1, 2, 3], 4, 1, 1)]
+    ws = workspace(max(spark_workspace_bytes_kv8(len(x), H, G, n) for x, H, G, n in shapes))
+    rng = random.Random(3)
+    ctx = [(_context(x, H, 16, SPARK_KV8_E4M3, i), _values(_gen(i), (len(x), H * G, n, D), torch.bfloat16), x, G)
+           for i, (x, H, G, n) in enumerate(shapes)]
+    alone = [_attend(q, kc, t, x, G)[0] for (kc, t), q, x, G in ctx]
+    for _ in range(20):
+        i = rng.randrange(len(ctx))
+        (kc, t), q, x, G = ctx[i]
+        out, _ = _attend(q, kc, t, x, G, ws=ws)
+        assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(alone[i], 7.0))
+    assert spark_device_status(ws) == 0
+
+
 def test_attn_peaked_scores():
     """Scores of some hundreds: the softmax is one token, or nearly."""
     _check_attn([300, 1000], 2, 4, 1, 16, SPARK_KV8_E4M3, torch.float32, spread=1.5)
