@@ -44,7 +44,6 @@ constexpr int kMaxStages = 24;             // stages of a CTA: 192 KB
 constexpr int kRingBytes = kMaxStages * kStageBytes;
 constexpr int kMinCtaSteps = 4;            // a CTA takes at least this many steps
 constexpr int kPScale = 6;                 // probabilities enter the second product times 2^6
-constexpr int kFlushSteps = 32;            // steps between two flushes of the running sums
 constexpr float kSlack = 8.f;              // log2 of how far a probability may pass its reference
 
 // What a stage's consumers need to know beside the codes.
@@ -56,17 +55,19 @@ struct __align__(16) StageMeta {
     int pad;
 };
 
-// Workspace: header, one counter per CTA (zero between calls), then the
-// partials of teams and of CTAs: acc [slot][rows][128] fp32, and (m, l)
-// [slot][rows][2].  Along the line the team and the pair only grow, so team +
-// pair numbers a team's partial of a pair uniquely, and CTA + pair a CTA's.
+// Workspace: header, one counter per CTA (zero between calls), the warps'
+// flushed sums ([warp][9 * kN][lane] float4), then the partials of teams and
+// of CTAs: acc [slot][rows][128] fp32, and (m, l) [slot][rows][2].  Along the
+// line the team and the pair only grow, so team + pair numbers a team's
+// partial of a pair uniquely, and CTA + pair a CTA's.
 static size_t attn_counter_bytes(int num_sms) { return ((size_t)num_sms * 4 + 255) / 256 * 256; }
+constexpr size_t kFlushBytes = 8 * 2 * 9 * 32 * sizeof(float4);  // of a CTA: 8 warps with two 8-row groups (12 with one need less)
 static long attn_team_slots(long pairs, int num_sms) { return (long)num_sms * kMaxTeams + pairs; }
 
 size_t attn_kv8_workspace(int B, int Hkv, int rows, int num_sms) {
     const long pairs = (long)B * Hkv;
     const size_t slots = (size_t)(attn_team_slots(pairs, num_sms) + num_sms + pairs);
-    return kWsHeader + attn_counter_bytes(num_sms) + slots * rows * (kD + 2) * sizeof(float);
+    return kWsHeader + attn_counter_bytes(num_sms) + num_sms * kFlushBytes + slots * rows * (kD + 2) * sizeof(float);
 }
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *tm, int row, uint32_t bar) {
@@ -192,6 +193,7 @@ struct AttnArgs {
     int table_cap, B, rows, G, n_q, team_warps, n_stages;
     float *out;
     uint32_t *ws, *counter;
+    float4 *flush;          // flushed sums
     float *acc, *ml;        // team partials
     float *acc_c, *ml_c;    // CTA partials
 };
@@ -292,6 +294,11 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     constexpr int kN = kNT ? kNT : 1;              // 8-row groups
     constexpr int kRows = kNT ? 8 * kNT : 4;       // query rows of a warp
     constexpr int kQ = sizeof(E) == 4 ? 2 : 1;     // fp16 halves of a query
+    // Steps between two flushes of the running sums: 64 products added to each
+    // sum (two a step where P's halves share a product, else four).  32 steps in
+    // the second case left errors of 1.4e-6 (fp32 sums: 1.3e-6, 16 steps: 7e-7);
+    // 12, 16, 24 and 32 steps took 78.1, 76.5, 75.8 and 75.1 us of a verify step.
+    constexpr int kFlushSteps = kNT ? 16 : 32;
     extern __shared__ unsigned char sm_raw[];
     __shared__ int before[kAtThreads + 1];   // steps (of one kv head) before each thread's rows
     __shared__ int wsum[kAtThreads / 32];
@@ -513,14 +520,44 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     // The running sums leave the registers: at the end of a pair, and every
     // kFlushSteps steps on the way.  The tensor cores cut off what they add up
     // (towards zero), which over 110 steps grew to 4e-6 of the result and would
-    // go on growing; a flush puts what has come together into the team's partial
-    // in global memory and starts the sums at zero, and the next one adds it to
-    // theirs in fp32.
+    // go on growing; a flush writes the sums to global memory, lane by lane, and
+    // starts them at zero, and the next one adds what was written in fp32.
     bool flushed = false;
     auto put_sums = [&](bool last, bool on_the_way) {
+        if (flushed || on_the_way) {
+            float4 *mine = a.flush + (size_t)(blockIdx.x * kAtWarps + warp) * (9 * kN * 32) + lane;
+#pragma unroll
+            for (int t = 0; t < kN; ++t, mine += 9 * 32) {
+                if (flushed) {
+                    float4 v[8];  // all loads before the first use
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __ldcg(mine + j * 32);
+                    const float4 was = __ldcg(mine + 8 * 32);
+                    const float k0 = was.x == -INFINITY ? 0.f : exp2_approx(was.x - m[t][0]);
+                    const float k1 = was.y == -INFINITY ? 0.f : exp2_approx(was.y - m[t][1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[t][j][0] += v[j].x * k0 * E_inv;
+                        o[t][j][1] += v[j].y * k1 * E_inv;
+                        o[t][j][2] += v[j].z * k0 * E_inv;
+                        o[t][j][3] += v[j].w * k1 * E_inv;
+                    }
+                }
+                if (on_the_way) {
+                    const float f = E_top * exp2_int(-kPScale);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        __stcg(mine + j * 32, make_float4(o[t][j][0] * f, o[t][j][1] * f, o[t][j][2] * f, o[t][j][3] * f));
+                        o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+                    }
+                    __stcg(mine + 8 * 32, make_float4(m[t][0], m[t][1], 0.f, 0.f));
+                }
+            }
+            flushed = on_the_way;
+            if (on_the_way) return;
+        }
         const long bh = (long)b * Hkv + h;
-        const bool whole = starts_pair && ends_pair && !on_the_way;
-        last = last && !on_the_way;
+        const bool whole = starts_pair && ends_pair;
         // A partial of the stretch's last pair goes to the team's own part of
         // the ring, which it has read by now; one of its first pair, with others
         // behind it, to global memory.
@@ -533,31 +570,13 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 s += __shfl_xor_sync(0xffffffffu, s, 4);
                 s += __shfl_xor_sync(0xffffffffu, s, 8);
                 s += __shfl_xor_sync(0xffffffffu, s, 16);
-                if (!on_the_way) l[t][j] = s;  // (a lane's own tokens until then)
+                l[t][j] = s;
             }
             if (kNT == 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[t][j][i] += __shfl_xor_sync(0xffffffffu, o[t][j][i], 2);
-            }
-            if (flushed) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (qi[t][j] >= nn) continue;
-                    const int row = wt * kRows + (kNT ? t * 8 + 2 * c + j : (2 * c + j) & 3);
-                    const size_t at = (size_t)(tm + bh) * a.rows + row;
-                    const float was = __ldcg(a.ml + at * 2), keep = was == -INFINITY ? 0.f : exp2_approx(was - m[t][j]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.acc + at * kD + g * 16) + i);
-                        o[t][2 * i][j] += v.x * keep * E_inv;
-                        o[t][2 * i][2 + j] += v.y * keep * E_inv;
-                        o[t][2 * i + 1][j] += v.z * keep * E_inv;
-                        o[t][2 * i + 1][2 + j] += v.w * keep * E_inv;
-                    }
-                }
-                __syncwarp();  // every lane has read the old partial
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -581,12 +600,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                         make_float4(o[t][2 * i][j] * f, o[t][2 * i][2 + j] * f, o[t][2 * i + 1][j] * f,
                                     o[t][2 * i + 1][2 + j] * f);
             }
-            if (on_the_way) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
-            }
         }
-        flushed = on_the_way;
     };
 
     // One loop fills the ring (it < 0), consumes the steps, and ends the last
@@ -1070,7 +1084,8 @@ cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, 
     const long pairs = (long)B * kc.Hkv;
     const size_t team_rows = (size_t)attn_team_slots(pairs, num_sms) * a.rows;
     const size_t cta_rows = (size_t)(num_sms + pairs) * a.rows;
-    a.acc = reinterpret_cast<float *>(w + kWsHeader + attn_counter_bytes(num_sms));
+    a.flush = reinterpret_cast<float4 *>(w + kWsHeader + attn_counter_bytes(num_sms));
+    a.acc = reinterpret_cast<float *>(w + kWsHeader + attn_counter_bytes(num_sms) + num_sms * kFlushBytes);
     a.acc_c = a.acc + team_rows * kD;
     a.ml = a.acc_c + cta_rows * kD;
     a.ml_c = a.ml + team_rows * 2;
