@@ -1,11 +1,12 @@
 // Attention over the paged 8-bit cache (spark_decode_attn_kv8).
 //
-// Split-K flash decoding.  The tokens of all (row, kv head) pairs, 32 to a
-// step, form one line of steps; each team of warps takes an equal stretch of
-// it, whatever the rows' lengths, and walks it with a ring of shared-memory
-// stages that TMA fills (keys and values of one step, 8 KB).  A stretch that
-// covers a pair wholly writes its output; the others leave (m, l, acc)
-// partials that a second kernel merges in order.
+// Split-K flash decoding in one launch, one CTA per SM.  The tokens of all
+// (row, kv head) pairs, 32 to a step, form one line of steps, row after row;
+// each CTA takes an equal stretch of it and each of its teams an equal part of
+// that, whatever the rows' lengths (48 rows of 17 to 32768 tokens run at the
+// rate of equal ones).  A team is as many warps as the query rows need, and
+// keeps a ring of stages that TMA fills (keys and values of a step, 8 KB, in
+// the 128-byte swizzle, which makes every fragment load below conflict-free).
 //
 // Per step and warp, tensor cores (m16n8k16, fp16 in, fp32 out):
 //   S^T[token][row]    = K[token][channel] . q^T       codes are exact in fp16
@@ -14,15 +15,30 @@
 // probabilities, so codes are only converted, never scaled.  A query row is
 // brought to [2^13, 2^14) by a power of two: bf16 is then exact in fp16
 // (elements 2^-27 below the row's largest lose bits), fp32 goes in as two
-// fp16 halves.  P is multiplied by 2^14 and by the page's value scale over a
-// power of two at or above every scale seen so far, and enters as two fp16
-// halves (22 bits, down to 2^-38 of the largest weight), so the result is
-// that of fp32 arithmetic.  The codes of values are paired by token with byte
-// permutes in registers (the transpose that the second product needs), P is
-// transposed by movmatrix; nothing else crosses lanes but the row maxima.
+// fp16 halves.  P is multiplied by 2^6 and by the page's value scale over a
+// power of two above every scale seen so far, and enters as two fp16 halves
+// (22 bits, down to 2^-31 of the largest weight), so the result is that of
+// fp32 arithmetic.  The codes of values are paired by token with byte permutes
+// in registers (the transpose that the second product needs), P is transposed
+// by movmatrix; nothing else crosses lanes but the row maxima.
 //
-// Bound by memory: 256 bytes per token and kv head against about 4.5
-// warp-instructions a byte-lane budget of 700 issue slots per 16 tokens.
+// A pair that one team has wholly is written at once.  Of others the teams
+// leave (m, l, acc) partials, which their CTA merges from shared memory; where
+// a pair crosses CTAs, the last of them to finish merges the CTAs' partials,
+// always in their order, so that results do not depend on timing.
+//
+// tcgen05 was not taken: a decode step has 4 to 16 query rows per kv head,
+// and codes would have to go through registers and back to shared memory as
+// fp16 first.  Legacy matrix instructions take their operands from registers,
+// where the codes are converted anyway, and are 17 % busy at 4 rows.
+//
+// Bound, from the profile: at up to 8 rows by memory while the ring is full
+// (about 23 bytes a clock and SM, 90 % of the copy rate between the first
+// stage's arrival and the last step), with 2.6 us before it (lengths, their
+// sum, table, pages: four dependent reads) and 4 to 8 us behind it (slowest
+// SM, merges).  At 16 rows by dependent-issue latency: 255 registers leave 8
+// warps, issue slots are 35 % used, and 78 us of 4 verified tokens compare
+// with 41 us of memory time.
 #include <cuda.h>  // CUtensorMap and its enums (the encoder is fetched at run time)
 
 #include "kv8.cuh"
@@ -32,7 +48,8 @@ namespace spark {
 bool make_kv8_map(CUtensorMap *tm, const void *codes, long rows, int box_rows);
 
 // Warps of a CTA, for a kernel whose warps work on kNT groups of 8 query rows
-// (168 or 255 registers a thread).
+// (168 or 255 registers a thread).  8 warps instead of 12 at kNT = 0 and 1: 3 to
+// 5 % slower; 12 at kNT = 2: spills, 109 us instead of 78.
 constexpr int kMaxTeams = 12;
 template <int kNT> struct AtGeom {
     static constexpr int kWarps = kNT == 2 ? 8 : 12;

@@ -13,6 +13,10 @@
 // a second launch for the sum.  lens_out may be lens and taken_out may be
 // taken (a replayed graph advances them in place): they are then written by
 // the last CTA to finish, when every other one has read them.
+//
+// Bound by latency: a launch, the lengths, the pages (three dependent reads),
+// 5 us of GPU time for 64 rows and 8 us for 2 M slots (9 MB, 1.4 us at the copy
+// rate); back to back a call is its 8 us of host time.
 #include "spark_internal.cuh"
 
 namespace spark {
