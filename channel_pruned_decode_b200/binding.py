@@ -439,7 +439,9 @@ class KV8Cache:
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
     """The library sees bare pointers: a tensor of another type, shape, layout
-    or device than the call needs is refused here."""
+    or device than the call needs is refused here.  (The calls below first test
+    all their tensors in one expression, which costs a decode step's small calls
+    a quarter of a microsecond a tensor, and come here only to say what is wrong.)"""
     if t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} needed, got {t.dtype}")
     if t.shape != shape:
@@ -450,10 +452,9 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
         raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {device}")
 
 
-def _fits(t: torch.Tensor, dtype, shape, index: int) -> bool:
-    """_need's checks in the few hundred nanoseconds that a decode step's calls
-    can spare for each tensor; on False, _need says what is wrong."""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
+def _need_ws(ws: torch.Tensor, device) -> None:
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: must be contiguous and on {device}")
 
 
 def _launch_stream(index: int, stream) -> int | None:
@@ -477,16 +478,20 @@ def spark_pages_extend(lens: torch.Tensor, n_new: torch.Tensor, page: int, pool:
                        ws: torch.Tensor, stream=None) -> None:
     """Pages for each row's n_new tokens (table [B, cap] and taken_out) and
     their slots [B, n_cap]; lens_out / taken_out may be lens / taken."""
-    i32, index = torch.int32, lens.get_device()
-    B, cap, n_cap, n_pages = lens.shape[0], table.shape[-1], slots.shape[-1], pool.shape[0]
-    row, one = (B,), (1,)
-    if not (_fits(lens, i32, row, index) and _fits(n_new, i32, row, index) and _fits(pool, i32, (n_pages,), index)
-            and _fits(taken, i32, one, index) and _fits(table, i32, (B, cap), index)
-            and _fits(slots, i32, (B, n_cap), index) and _fits(lens_out, i32, row, index)
-            and _fits(taken_out, i32, one, index)):
-        for t, name, shape in ((lens, "lens", row), (n_new, "n_new", row), (pool, "pool", (n_pages,)),
-                               (taken, "taken", one), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
-                               (lens_out, "lens_out", row), (taken_out, "taken_out", one)):
+    i32, index, B = torch.int32, lens.get_device(), lens.numel()
+    (rows, cap), (rows_s, n_cap), n_pages = table.shape, slots.shape, pool.numel()
+    if not (lens.dtype is n_new.dtype is pool.dtype is taken.dtype is table.dtype is slots.dtype is lens_out.dtype
+            is taken_out.dtype is i32 and n_new.numel() == lens_out.numel() == rows == rows_s == B
+            and taken.numel() == taken_out.numel() == 1
+            and lens.is_contiguous() and n_new.is_contiguous() and pool.is_contiguous() and table.is_contiguous()
+            and slots.is_contiguous() and lens_out.is_contiguous()
+            and n_new.get_device() == pool.get_device() == taken.get_device() == table.get_device()
+            == slots.get_device() == lens_out.get_device() == taken_out.get_device() == ws.get_device() == index
+            and ws.is_contiguous()):
+        _need_ws(ws, lens.device)
+        for t, name, shape in ((lens, "lens", (B,)), (n_new, "n_new", (B,)), (pool, "pool", (n_pages,)),
+                               (taken, "taken", (1,)), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
+                               (lens_out, "lens_out", (B,)), (taken_out, "taken_out", (1,))):
             _need(t, name, i32, shape, lens.device)
     rc = lib().spark_pages_extend(lens.data_ptr(), n_new.data_ptr(), B, page, pool.data_ptr(), n_pages,
                                   taken.data_ptr(), table.data_ptr(), cap, n_cap, slots.data_ptr(),
@@ -501,15 +506,19 @@ def spark_pages_trim(lens: torch.Tensor, keep: torch.Tensor, page: int, pool: to
                      stream=None) -> None:
     """Cut each row to its first keep tokens and give the pages behind them
     back to the pool; lens_out / taken_out may be lens / taken."""
-    i32, index = torch.int32, lens.get_device()
-    B, cap, n_pages = lens.shape[0], table.shape[-1], pool.shape[0]
-    row, one = (B,), (1,)
-    if not (_fits(lens, i32, row, index) and _fits(keep, i32, row, index) and _fits(pool, i32, (n_pages,), index)
-            and _fits(taken, i32, one, index) and _fits(table, i32, (B, cap), index)
-            and _fits(lens_out, i32, row, index) and _fits(taken_out, i32, one, index)):
-        for t, name, shape in ((lens, "lens", row), (keep, "keep", row), (pool, "pool", (n_pages,)),
-                               (taken, "taken", one), (table, "table", (B, cap)), (lens_out, "lens_out", row),
-                               (taken_out, "taken_out", one)):
+    i32, index, B = torch.int32, lens.get_device(), lens.numel()
+    (rows, cap), n_pages = table.shape, pool.numel()
+    if not (lens.dtype is keep.dtype is pool.dtype is taken.dtype is table.dtype is lens_out.dtype
+            is taken_out.dtype is i32 and keep.numel() == lens_out.numel() == rows == B
+            and taken.numel() == taken_out.numel() == 1
+            and lens.is_contiguous() and keep.is_contiguous() and pool.is_contiguous() and table.is_contiguous()
+            and lens_out.is_contiguous()
+            and keep.get_device() == pool.get_device() == taken.get_device() == table.get_device()
+            == lens_out.get_device() == taken_out.get_device() == ws.get_device() == index and ws.is_contiguous()):
+        _need_ws(ws, lens.device)
+        for t, name, shape in ((lens, "lens", (B,)), (keep, "keep", (B,)), (pool, "pool", (n_pages,)),
+                               (taken, "taken", (1,)), (table, "table", (B, cap)), (lens_out, "lens_out", (B,)),
+                               (taken_out, "taken_out", (1,))):
             _need(t, name, i32, shape, lens.device)
     rc = lib().spark_pages_trim(lens.data_ptr(), keep.data_ptr(), B, page, pool.data_ptr(), n_pages,
                                 taken.data_ptr(), table.data_ptr(), cap, lens_out.data_ptr(), taken_out.data_ptr(),
@@ -525,8 +534,11 @@ def spark_kv8_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tens
     B, n_cap = slots.shape
     index, dt = kc.index, k_new.dtype
     shape = (B, kc.Hkv, kc.D) if n_cap == 1 and k_new.dim() == 3 else (B, kc.Hkv, n_cap, kc.D)
-    if not (_fits(k_new, dt, shape, index) and _fits(v_new, dt, shape, index)
-            and _fits(slots, torch.int32, (B, n_cap), index)):
+    if not (k_new.shape == shape and v_new.shape == shape and v_new.dtype is dt and slots.dtype is torch.int32
+            and k_new.is_contiguous() and v_new.is_contiguous() and slots.is_contiguous()
+            and k_new.get_device() == v_new.get_device() == slots.get_device() == ws.get_device() == index
+            and ws.is_contiguous()):
+        _need_ws(ws, kc.k.device)
         _need(k_new, "k_new", dt, shape, kc.k.device)
         _need(v_new, "v_new", dt, shape, kc.k.device)
         _need(slots, "slots", torch.int32, (B, n_cap), kc.k.device)
@@ -547,17 +559,21 @@ def spark_decode_attn_kv8(q: torch.Tensor, kc: KV8Cache, table: torch.Tensor, le
         shape = (B, kc.Hkv * G, n_q, kc.D)
     else:
         n_q, shape = 1, (B, kc.Hkv * G, kc.D)
-    row = (B,)
-    if not (_fits(q, dt, shape, index) and _fits(out, torch.float32, shape, index)
-            and _fits(table, i32, (B, cap), index) and _fits(lens, i32, row, index)
-            and (n_new is None or _fits(n_new, i32, row, index))):
+    if not (q.shape == shape and out.shape == shape and out.dtype is torch.float32
+            and table.dtype is lens.dtype is i32 and lens.numel() == B
+            and q.is_contiguous() and out.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
+            and q.get_device() == out.get_device() == table.get_device() == lens.get_device() == ws.get_device() == index
+            and ws.is_contiguous()
+            and (n_new is None or (n_new.dtype is i32 and n_new.numel() == B and n_new.is_contiguous()
+                                   and n_new.get_device() == index))):
         dev = kc.k.device
+        _need_ws(ws, dev)
         _need(q, "q", dt, shape, dev)
         _need(out, "out", torch.float32, shape, dev)
         _need(table, "table", i32, (B, cap), dev)
-        _need(lens, "lens", i32, row, dev)
+        _need(lens, "lens", i32, (B,), dev)
         if n_new is not None:
-            _need(n_new, "n_new", i32, row, dev)
+            _need(n_new, "n_new", i32, (B,), dev)
     rc = lib().spark_decode_attn_kv8(q.data_ptr(), _dtype_code(dt), kc.ref, table.data_ptr(), cap, lens.data_ptr(),
                                      None if n_new is None else n_new.data_ptr(), B, G, n_q, out.data_ptr(),
                                      ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))

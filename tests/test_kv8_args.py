@@ -138,6 +138,11 @@ def test_binding_refuses_wrong_tensors():
         B.spark_decode_attn_kv8(q, kc, i32(3, 4), i32(3), 4, out, ws, n_new=i32(3).long())
     with pytest.raises(ValueError, match="current CUDA device"):
         B.spark_pages_extend(i32(3), i32(3), 16, i32(9), i32(1), i32(3, 4), i32(3, 5), i32(3), i32(1), ws)
+    with pytest.raises(ValueError, match="ws"):
+        B.spark_pages_extend(i32(3), i32(3), 16, i32(9), i32(1), i32(3, 4), i32(3, 5), i32(3), i32(1),
+                             torch.zeros((64, 8), dtype=torch.uint8).t())
+    with pytest.raises(ValueError, match="ws"):
+        B.spark_kv8_append(x, x, slots, kc, torch.zeros((64, 8), dtype=torch.uint8).t())
     with pytest.raises(ValueError, match="taken"):
         B.spark_pages_extend(i32(3), i32(3), 16, i32(9), i32(2), i32(3, 4), i32(3, 5), i32(3), i32(1), ws)
     with pytest.raises(ValueError, match="table"):
