@@ -78,7 +78,8 @@ struct __align__(16) StageMeta {
 // line the team and the pair only grow, so team + pair numbers a team's
 // partial of a pair uniquely, and CTA + pair a CTA's.
 static size_t attn_counter_bytes(int num_sms) { return ((size_t)num_sms * 4 + 255) / 256 * 256; }
-constexpr size_t kFlushBytes = 8 * 2 * 9 * 32 * sizeof(float4);  // of a CTA: 8 warps with two 8-row groups (12 with one need less)
+// of a CTA: 8 warps with two 8-row groups (12 with one need less)
+constexpr size_t kFlushBytes = 8 * 2 * 9 * 32 * sizeof(float4);
 static long attn_team_slots(long pairs, int num_sms) { return (long)num_sms * kMaxTeams + pairs; }
 
 size_t attn_kv8_workspace(int B, int Hkv, int rows, int num_sms) {
@@ -630,227 +631,227 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll 1
     for (int it = steps > 0 ? -ns : 1; it <= steps; ++it) {
         if (it >= 0) {
-        StageMeta mt;
-        if (it < steps) {
-            // a wait that ran out does not leave the loop (lanes would part there):
-            // the rest is computed from what the stages hold, and thrown away
-            if (!failed) failed = !wait_warp(smem_u32(&full[st0 + st]), parity);
-            mt = meta[st0 + st];
-        }
-        const bool over = it == steps || (!failed && uniform(mt.b != b || mt.h != h));
-        if (over || since == kFlushSteps) {
-            since = 0;
-            if (it == steps && opaque(tw) > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tw * 32) : "memory");
-            if (uniform(b >= 0) && !failed) put_sums(it == steps, !over);
-            if (it == steps) break;
-        }
-        if (over) {
-            begin_pair(mt);
-            if (wt == 0 && lane == 0) {  // for the merge
-                const int i = it == 0 ? 0 : 1;
-                stretch[team].pair[i] = stretch[team].pair[1] = b * Hkv + h;
-                stretch[team].x0[i] = stretch[team].x0[1] = from + it - mt.s;
-                stretch[team].n[i] = stretch[team].n[1] = mt.n_steps;
-                stretch[team].nn[i] = stretch[team].nn[1] = nn;
+            StageMeta mt;
+            if (it < steps) {
+                // a wait that ran out does not leave the loop (lanes would part there):
+                // the rest is computed from what the stages hold, and thrown away
+                if (!failed) failed = !wait_warp(smem_u32(&full[st0 + st]), parity);
+                mt = meta[st0 + st];
             }
-        }
-        ++since;
-        ends_pair = mt.s + 1 == mt.n_steps;
-        const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
-        const int t0 = uniform(mt.s) * kStep;
-
-        // scores
-        float s[kN][2][4];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-            for (int t = 0; t < kN; ++t) s[t][hf][0] = s[t][hf][1] = s[t][hf][2] = s[t][hf][3] = 0.f;
-            const uint32_t r0 = kb + (uint32_t)(hf * 16 + g) * kD;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t x = (uint32_t)((2 * c + i) ^ g) << 4;
-                const uint4 u = lds128(r0 + x), w = lds128(r0 + 8 * kD + x);
-                const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a0, a1, a2, a3;
-                    expand4<kType>(uu[j], a0, a2);
-                    expand4<kType>(ww[j], a1, a3);
-                    const int f = (i * 4 + j) * 2;
-#pragma unroll
-                    for (int t = 0; t < kN; ++t)
-#pragma unroll
-                        for (int y = 0; y < kQ; ++y)
-                            mma16816(s[t][hf], a0, a1, a2, a3, qh[y][t][f], qh[y][t][f + 1]);
+            const bool over = it == steps || (!failed && uniform(mt.b != b || mt.h != h));
+            if (over || since == kFlushSteps) {
+                since = 0;
+                if (it == steps && opaque(tw) > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tw * 32) : "memory");
+                if (uniform(b >= 0) && !failed) put_sums(it == steps, !over);
+                if (it == steps) break;
+            }
+            if (over) {
+                begin_pair(mt);
+                if (wt == 0 && lane == 0) {  // for the merge
+                    const int i = it == 0 ? 0 : 1;
+                    stretch[team].pair[i] = stretch[team].pair[1] = b * Hkv + h;
+                    stretch[team].x0[i] = stretch[team].x0[1] = from + it - mt.s;
+                    stretch[team].n[i] = stretch[team].n[1] = mt.n_steps;
+                    stretch[team].nn[i] = stretch[team].nn[1] = nn;
                 }
             }
-        }
-        // places without a token and tokens behind a query's own
-        const bool holes = uniform(mt.nv[0] < 16 || mt.nv[1] < 16);
-        const bool edge = holes || t0 + kStep > first_full;
-        bool hide = false;
-        if (edge) {
+            ++since;
+            ends_pair = mt.s + 1 == mt.n_steps;
+            const uint32_t kb = base + (uint32_t)st * kStageBytes, vb = kb + kStep * kD;
+            const int t0 = uniform(mt.s) * kStep;
+
+            // scores
+            float s[kN][2][4];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                for (int t = 0; t < kN; ++t) s[t][hf][0] = s[t][hf][1] = s[t][hf][2] = s[t][hf][3] = 0.f;
+                const uint32_t r0 = kb + (uint32_t)(hf * 16 + g) * kD;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x = (uint32_t)((2 * c + i) ^ g) << 4;
+                    const uint4 u = lds128(r0 + x), w = lds128(r0 + 8 * kD + x);
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a0, a1, a2, a3;
+                        expand4<kType>(uu[j], a0, a2);
+                        expand4<kType>(ww[j], a1, a3);
+                        const int f = (i * 4 + j) * 2;
+#pragma unroll
+                        for (int t = 0; t < kN; ++t)
+#pragma unroll
+                            for (int y = 0; y < kQ; ++y)
+                                mma16816(s[t][hf], a0, a1, a2, a3, qh[y][t][f], qh[y][t][f + 1]);
+                    }
+                }
+            }
+            // places without a token and tokens behind a query's own
+            const bool holes = uniform(mt.nv[0] < 16 || mt.nv[1] < 16);
+            const bool edge = holes || t0 + kStep > first_full;
+            bool hide = false;
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < kN; ++t)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int in = g + 8 * (i >> 1);
+                            if (in >= mt.nv[hf] || t0 + hf * 16 + in > lim[t][i & 1]) s[t][hf][i] = -INFINITY;
+                        }
+                // Places without a token may hold anything, NaN codes too: their
+                // values become zeros before the second product meets them.
+                if (holes) {
+#pragma unroll 1
+                    for (int i = lane; i < kStep * 8; i += 32) {
+                        const int row = i >> 3;
+                        if ((row & 15) >= (row < 16 ? mt.nv[0] : mt.nv[1]))
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (uint32_t)i * 16), "r"(0u)
+                                         : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                // A token that some of the queries do not see takes part in the second
+                // product with p = 0 for them: where its value is NaN, the queries that
+                // see it get their NaN here and the product a zero.
+                if (kType == SPARK_KV8_E4M3 && opaque(a.n_q) > 1) {
+#pragma unroll 1
+                    for (int i = max(first_full - t0, 0); i < kStep; ++i) {
+                        // (places without a token are zeros by now)
+                        const uint4 w = lds128(vb + (uint32_t)i * kD + ((uint32_t)(g ^ (i & 7)) << 4));
+                        const uint32_t ww[4] = {nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w)};
+                        if (!__any_sync(0xffffffffu, (ww[0] | ww[1] | ww[2] | ww[3]) != 0)) continue;
+                        hide = true;
+#pragma unroll
+                        for (int t = 0; t < kN; ++t)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    if (((ww[j / 4] >> (8 * (j % 4))) & 0xffu) && t0 + i <= lim[t][y])
+                                        o[t][j / 2][(j & 1) * 2 + y] = __int_as_float(0x7fffffff);
+                    }
+                }
+            }
+            // The reference m of a row's probabilities (in units of log2) is its
+            // largest score so far, but follows it only when that is more than
+            // kSlack above: the sums take any reference, and most steps then
+            // need no maximum across lanes and no rescaling.
+            float f[kN][2][2];
+            bool move = false;
 #pragma unroll
             for (int t = 0; t < kN; ++t)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int in = g + 8 * (i >> 1);
-                        if (in >= mt.nv[hf] || t0 + hf * 16 + in > lim[t][i & 1]) s[t][hf][i] = -INFINITY;
-                    }
-            // Places without a token may hold anything, NaN codes too: their
-            // values become zeros before the second product meets them.
-            if (holes) {
-#pragma unroll 1
-                for (int i = lane; i < kStep * 8; i += 32) {
-                    const int row = i >> 3;
-                    if ((row & 15) >= (row < 16 ? mt.nv[0] : mt.nv[1]))
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (uint32_t)i * 16), "r"(0u)
-                                     : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            // A token that some of the queries do not see takes part in the second
-            // product with p = 0 for them: where its value is NaN, the queries that
-            // see it get their NaN here and the product a zero.
-            if (kType == SPARK_KV8_E4M3 && opaque(a.n_q) > 1) {
-#pragma unroll 1
-                for (int i = max(first_full - t0, 0); i < kStep; ++i) {
-                    // (places without a token are zeros by now)
-                    const uint4 w = lds128(vb + (uint32_t)i * kD + ((uint32_t)(g ^ (i & 7)) << 4));
-                    const uint32_t ww[4] = {nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w)};
-                    if (!__any_sync(0xffffffffu, (ww[0] | ww[1] | ww[2] | ww[3]) != 0)) continue;
-                    hide = true;
-#pragma unroll
-                    for (int t = 0; t < kN; ++t)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                if (((ww[j / 4] >> (8 * (j % 4))) & 0xffu) && t0 + i <= lim[t][y])
-                                    o[t][j / 2][(j & 1) * 2 + y] = __int_as_float(0x7fffffff);
-                }
-            }
-        }
-        // The reference m of a row's probabilities (in units of log2) is its
-        // largest score so far, but follows it only when that is more than
-        // kSlack above: the sums take any reference, and most steps then
-        // need no maximum across lanes and no rescaling.
-        float f[kN][2][2];
-        bool move = false;
-#pragma unroll
-        for (int t = 0; t < kN; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                // above 0, so that an unseen place stays at -inf whatever its page's scale
-                f[t][0][j] = fmaxf(qf[t][j] * mt.ks[0], exp2_int(-126));
-                f[t][1][j] = fmaxf(qf[t][j] * mt.ks[1], exp2_int(-126));
-                const float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
-                                       fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
-                move |= mx > m[t][j] + kSlack;
-            }
-        const float vm = fmaxf(mt.vs[0], mt.vs[1]);
-        if (__any_sync(0xffffffffu, move || vm > E_top)) {
-            float grow = 1.f;
-            if (vm > E_top) {
-                const float top = __uint_as_float((__float_as_uint(vm) & 0x7f800000u) + 0x800000u);
-                grow = E_top / top;
-                E_top = top;
-                E_inv = exp2_int(kPScale) / top;
-            }
-#pragma unroll
-            for (int t = 0; t < kN; ++t) {
-                float al[2];
-#pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
-                                     fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[t][j], mx);
-                    al[j] = mn > m[t][j] ? exp2_approx(m[t][j] - mn) : 1.f;  // 0 from -inf
-                    m[t][j] = mn;
-                    l[t][j] *= al[j];
-                    al[j] *= grow;
+                    // above 0, so that an unseen place stays at -inf whatever its page's scale
+                    f[t][0][j] = fmaxf(qf[t][j] * mt.ks[0], exp2_int(-126));
+                    f[t][1][j] = fmaxf(qf[t][j] * mt.ks[1], exp2_int(-126));
+                    const float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
+                                           fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
+                    move |= mx > m[t][j] + kSlack;
+                }
+            const float vm = fmaxf(mt.vs[0], mt.vs[1]);
+            if (__any_sync(0xffffffffu, move || vm > E_top)) {
+                float grow = 1.f;
+                if (vm > E_top) {
+                    const float top = __uint_as_float((__float_as_uint(vm) & 0x7f800000u) + 0x800000u);
+                    grow = E_top / top;
+                    E_top = top;
+                    E_inv = exp2_int(kPScale) / top;
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    o[t][j][0] *= al[0];
-                    o[t][j][1] *= al[1];
-                    o[t][j][2] *= al[0];
-                    o[t][j][3] *= al[1];
-                }
-            }
-        }
-        // probabilities, their sums, and the second product
+                for (int t = 0; t < kN; ++t) {
+                    float al[2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const float cf = mt.vs[hf] * E_inv;
-            uint32_t ph[kN][2], pl_[kN][2];
+                    for (int j = 0; j < 2; ++j) {
+                        float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
+                                         fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mn = fmaxf(m[t][j], mx);
+                        al[j] = mn > m[t][j] ? exp2_approx(m[t][j] - mn) : 1.f;  // 0 from -inf
+                        m[t][j] = mn;
+                        l[t][j] *= al[j];
+                        al[j] *= grow;
+                    }
 #pragma unroll
-            for (int t = 0; t < kN; ++t) {
-                const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float p0 = exp2_approx(s[t][hf][2 * r] * f[t][hf][0] - m0);
-                    float p1 = exp2_approx(s[t][hf][2 * r + 1] * f[t][hf][1] - m1);
-                    l[t][0] += p0;
-                    l[t][1] += p1;
-                    p0 *= cf;
-                    p1 *= cf;
-                    const __half2 hi = __floats2half2_rn(p0, p1);
-                    const float2 back = __half22float2(hi);
-                    const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);
-                    const uint32_t lb = pack_half2(p0 - back.x, p1 - back.y);
-                    if (kNT == 0) {
-                        ph[t][r] = transpose8x8(c < 2 ? hb : lb);
-                    } else {
-                        ph[t][r] = transpose8x8(hb);
-                        pl_[t][r] = transpose8x8(lb);
+                    for (int j = 0; j < 8; ++j) {
+                        o[t][j][0] *= al[0];
+                        o[t][j][1] *= al[1];
+                        o[t][j][2] *= al[0];
+                        o[t][j][3] *= al[1];
                     }
                 }
             }
-            // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, channels 16 g .. 16 g + 15
-            uint4 w[4];
+            // probabilities, their sums, and the second product
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
-                w[i] = lds128(vb + (uint32_t)row * kD + ((uint32_t)(g ^ (row & 7)) << 4));
-            }
-            if (kType == SPARK_KV8_E4M3 && hide) {
-                __syncwarp();  // a branch, not predicates on the common path
+            for (int hf = 0; hf < 2; ++hf) {
+                const float cf = mt.vs[hf] * E_inv;
+                uint32_t ph[kN][2], pl_[kN][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (t0 + hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8 >= first_full)
-                        w[i] = make_uint4(w[i].x & ~nan_codes(w[i].x), w[i].y & ~nan_codes(w[i].y),
-                                          w[i].z & ~nan_codes(w[i].z), w[i].w & ~nan_codes(w[i].w));
-            }
-            const uint32_t ww[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
-                                       {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+                for (int t = 0; t < kN; ++t) {
+                    const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+                    for (int r = 0; r < 2; ++r) {
+                        float p0 = exp2_approx(s[t][hf][2 * r] * f[t][hf][0] - m0);
+                        float p1 = exp2_approx(s[t][hf][2 * r + 1] * f[t][hf][1] - m1);
+                        l[t][0] += p0;
+                        l[t][1] += p1;
+                        p0 *= cf;
+                        p1 *= cf;
+                        const __half2 hi = __floats2half2_rn(p0, p1);
+                        const float2 back = __half22float2(hi);
+                        const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);
+                        const uint32_t lb = pack_half2(p0 - back.x, p1 - back.y);
+                        if (kNT == 0) {
+                            ph[t][r] = transpose8x8(c < 2 ? hb : lb);
+                        } else {
+                            ph[t][r] = transpose8x8(hb);
+                            pl_[t][r] = transpose8x8(lb);
+                        }
+                    }
+                }
+                // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, channels 16 g .. 16 g + 15
+                uint4 w[4];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    uint32_t a0, a1, a2, a3;
-                    expand4<kType>(__byte_perm(ww[0][j], ww[1][j], y ? 0x7362 : 0x5140), a0, a1);
-                    expand4<kType>(__byte_perm(ww[2][j], ww[3][j], y ? 0x7362 : 0x5140), a2, a3);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
+                    w[i] = lds128(vb + (uint32_t)row * kD + ((uint32_t)(g ^ (row & 7)) << 4));
+                }
+                if (kType == SPARK_KV8_E4M3 && hide) {
+                    __syncwarp();  // a branch, not predicates on the common path
 #pragma unroll
-                    for (int t = 0; t < kN; ++t) {
-                        mma16816(o[t][2 * j + y], a0, a1, a2, a3, ph[t][0], ph[t][1]);
-                        if (kNT) mma16816(o[t][2 * j + y], a0, a1, a2, a3, pl_[t][0], pl_[t][1]);
+                    for (int i = 0; i < 4; ++i)
+                        if (t0 + hf * 16 + 2 * c + (i & 1) + (i >> 1) * 8 >= first_full)
+                            w[i] = make_uint4(w[i].x & ~nan_codes(w[i].x), w[i].y & ~nan_codes(w[i].y),
+                                              w[i].z & ~nan_codes(w[i].z), w[i].w & ~nan_codes(w[i].w));
+                }
+                const uint32_t ww[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
+                                           {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t a0, a1, a2, a3;
+                        expand4<kType>(__byte_perm(ww[0][j], ww[1][j], y ? 0x7362 : 0x5140), a0, a1);
+                        expand4<kType>(__byte_perm(ww[2][j], ww[3][j], y ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                        for (int t = 0; t < kN; ++t) {
+                            mma16816(o[t][2 * j + y], a0, a1, a2, a3, ph[t][0], ph[t][1]);
+                            if (kNT) mma16816(o[t][2 * j + y], a0, a1, a2, a3, pl_[t][0], pl_[t][1]);
+                        }
                     }
                 }
             }
-        }
-        __syncwarp();
-        if (opaque(tw) > 1 && lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
-        if (++st == ns) {
-            st = 0;
-            parity ^= 1;
-        }
+            __syncwarp();
+            if (opaque(tw) > 1 && lane == 0) mbar_arrive(smem_u32(&empty[st0 + st]));
+            if (++st == ns) {
+                st = 0;
+                parity ^= 1;
+            }
         }
         // A stage is free once every warp of the team has read it.  A team of
         // one refills it at once; a larger one refills the stage before, which
@@ -990,7 +991,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         }
     }
     __syncthreads();
-    float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + kAtWarps * kD;  // one (row, part) a warp where a row has several
+    // one (row, part) a warp where a row has several
+    float *sm_acc = reinterpret_cast<float *>(sm_raw), *sm_ml = sm_acc + kAtWarps * kD;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         const int pair = uniform(last_pair[k]);
@@ -1000,7 +1002,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll 1
         for (int row = mg_row; row < a.rows; row += kAtWarps) {
             const int i0 = mg_part * each, i1 = min(n, i0 + each);
-            if (a.n_q > 1 && row % a.n_q >= nn_p) continue;
+            if ((a.n_q > 1 ? row % a.n_q : 0) >= nn_p) continue;
             Merged r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
             for (int i = i0; i < i1; i += 8) {  // 8 at a time, all loads before the weights
@@ -1033,7 +1035,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         __syncthreads();
 #pragma unroll 1
         for (int row = warp; row < a.rows; row += kAtWarps) {
-            if (a.n_q > 1 && row % a.n_q >= nn_p) continue;
+            if ((a.n_q > 1 ? row % a.n_q : 0) >= nn_p) continue;
             Merged r;
             const float e = merge_weights(
                 lane < parts ? reinterpret_cast<const float2 *>(sm_ml)[row * parts + lane] : make_float2(-INFINITY, 0.f), r);

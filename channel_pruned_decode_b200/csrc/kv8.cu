@@ -202,84 +202,84 @@ __global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps
     }
 #pragma unroll 1
     for (int w = first; w < last; ++w) {
-    const int h = w >> 1;
-    const E *src = ((w & 1) ? v_new : k_new) + ((size_t)b * Hkv + h) * n_cap * kD;
-    uint8_t *codes = static_cast<uint8_t *>((w & 1) ? kc.v : kc.k);
-    float *scales = (w & 1) ? kc.v_scale : kc.k_scale;
-    Run r = run;
+        const int h = w >> 1;
+        const E *src = ((w & 1) ? v_new : k_new) + ((size_t)b * Hkv + h) * n_cap * kD;
+        uint8_t *codes = static_cast<uint8_t *>((w & 1) ? kc.v : kc.k);
+        float *scales = (w & 1) ? kc.v_scale : kc.k_scale;
+        Run r = run;
 #pragma unroll 1
-    while (r.n > 0) {
-        const int o = r.slot & (page - 1);
-        const size_t ph = (size_t)(r.slot / page) * Hkv + h;
-        uint8_t *dst = codes + ph * page * kD;
-        // this warp's tokens of the run: t0 ..
-        const int t0 = wt * kTokens, sub = lane / kRowLanes, col = lane % kRowLanes;
-        const bool whole = t0 + kTokens <= r.n;  // all of this warp's tokens are there
-        uint4 x[kLoads];
-        const float old = o > 0 ? scales[ph] : 0.f;
-        const uint4 *from = reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t0 + sub) * kD) + col;
-        if (whole) {
+        while (r.n > 0) {
+            const int o = r.slot & (page - 1);
+            const size_t ph = (size_t)(r.slot / page) * Hkv + h;
+            uint8_t *dst = codes + ph * page * kD;
+            // this warp's tokens of the run: t0 ..
+            const int t0 = wt * kTokens, sub = lane / kRowLanes, col = lane % kRowLanes;
+            const bool whole = t0 + kTokens <= r.n;  // all of this warp's tokens are there
+            uint4 x[kLoads];
+            const float old = o > 0 ? scales[ph] : 0.f;
+            const uint4 *from = reinterpret_cast<const uint4 *>(src + (size_t)(r.j + t0 + sub) * kD) + col;
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) x[i] = __ldcs(from + i * kPer * (kD / kVec));
-        } else {
+                for (int i = 0; i < kLoads; ++i) x[i] = __ldcs(from + i * kPer * (kD / kVec));
+            } else {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                x[i] = t0 + i * kPer + sub < r.n ? __ldcs(from + i * kPer * (kD / kVec)) : make_uint4(0, 0, 0, 0);
-        }
-        bool special;
-        float a = largest<E, kLoads>(x, &special);
-        if (tw > 1) {
-            team_sync(team, tw);  // the last run's maxima have been read
-            if (lane == 0) part[warp] = a;
-            team_sync(team, tw);
-            a = lane < tw ? part[team * tw + lane] : 0.f;
-            a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-        }
-        const int ex = kv8_exponent<kType>(a);
-        const float need = exp2_int(ex);
-        special |= ex == kKv8MaxExp;  // values may lie beyond the largest code
-        const bool keeps = o > 0 && old >= need;
-        const float inv = keeps ? 1.0f / old : exp2_int(-ex);
-        if (o > 0 && !keeps) {  // the page's codes move to the larger scale
-            const float ratio = old * inv;
+                for (int i = 0; i < kLoads; ++i)
+                    x[i] = t0 + i * kPer + sub < r.n ? __ldcs(from + i * kPer * (kD / kVec)) : make_uint4(0, 0, 0, 0);
+            }
+            bool special;
+            float a = largest<E, kLoads>(x, &special);
+            if (tw > 1) {
+                team_sync(team, tw);  // the last run's maxima have been read
+                if (lane == 0) part[warp] = a;
+                team_sync(team, tw);
+                a = lane < tw ? part[team * tw + lane] : 0.f;
+                a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+            }
+            const int ex = kv8_exponent<kType>(a);
+            const float need = exp2_int(ex);
+            special |= ex == kKv8MaxExp;  // values may lie beyond the largest code
+            const bool keeps = o > 0 && old >= need;
+            const float inv = keeps ? 1.0f / old : exp2_int(-ex);
+            if (o > 0 && !keeps) {  // the page's codes move to the larger scale
+                const float ratio = old * inv;
 #pragma unroll 1
-            for (int i = wt * 32 + lane; i < o * (kD / 16); i += tw * 32) {
-                uint4 w = *(reinterpret_cast<const uint4 *>(dst) + i);
+                for (int i = wt * 32 + lane; i < o * (kD / 16); i += tw * 32) {
+                    uint4 w = *(reinterpret_cast<const uint4 *>(dst) + i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t &c = (&w.x)[j];
-                    const float2 lo = __half22float2(kv8_decode2<kType>(c & 0xffffu));
-                    const float2 hi = __half22float2(kv8_decode2<kType>(c >> 16));
-                    c = kv8_encode2<kType>(lo.x * ratio, lo.y * ratio) |
-                        (kv8_encode2<kType>(hi.x * ratio, hi.y * ratio) << 16);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t &c = (&w.x)[j];
+                        const float2 lo = __half22float2(kv8_decode2<kType>(c & 0xffffu));
+                        const float2 hi = __half22float2(kv8_decode2<kType>(c >> 16));
+                        c = kv8_encode2<kType>(lo.x * ratio, lo.y * ratio) |
+                            (kv8_encode2<kType>(hi.x * ratio, hi.y * ratio) << 16);
+                    }
+                    *(reinterpret_cast<uint4 *>(dst) + i) = w;
                 }
-                *(reinterpret_cast<uint4 *>(dst) + i) = w;
             }
-        }
-        if (wt == 0 && lane == 0 && !keeps) scales[ph] = need;
-        uint8_t *to = dst + (size_t)(o + t0 + sub) * kD + col * kVec;
+            if (wt == 0 && lane == 0 && !keeps) scales[ph] = need;
+            uint8_t *to = dst + (size_t)(o + t0 + sub) * kD + col * kVec;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t c[kVec / 4];
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t c[kVec / 4];
 #pragma unroll
-            for (int j = 0; j < kVec / 4; ++j) {
-                float f[4];
-                unpack4<E>(x[i], j, f);
-                c[j] = encode4<kType>(f, inv, special);
+                for (int j = 0; j < kVec / 4; ++j) {
+                    float f[4];
+                    unpack4<E>(x[i], j, f);
+                    c[j] = encode4<kType>(f, inv, special);
+                }
+                if (whole || t0 + i * kPer + sub < r.n) {
+                    if (kVec == 8)
+                        *reinterpret_cast<uint2 *>(to + i * kPer * kD) = make_uint2(c[0], c[kVec / 4 - 1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(to + i * kPer * kD) = c[0];
+                }
             }
-            if (whole || t0 + i * kPer + sub < r.n) {
-                if (kVec == 8)
-                    *reinterpret_cast<uint2 *>(to + i * kPer * kD) = make_uint2(c[0], c[kVec / 4 - 1]);
-                else
-                    *reinterpret_cast<uint32_t *>(to + i * kPer * kD) = c[0];
-            }
+            if (plain) break;
+            // a later run of this piece may lie in the same page
+            __threadfence_block();
+            team_sync(team, tw);
+            r = next_run(row, r.j + r.n, end, n_cap, page, n_slots, &bad);
         }
-        if (plain) break;
-        // a later run of this piece may lie in the same page
-        __threadfence_block();
-        team_sync(team, tw);
-        r = next_run(row, r.j + r.n, end, n_cap, page, n_slots, &bad);
-    }
     }
     if (bad) atomicOr(status, kDevBadArg);
 }

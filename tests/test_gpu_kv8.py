@@ -262,6 +262,14 @@ def test_attn_long_and_many(H, lens):
     _check_attn(lens, H, 8, 2, 64, SPARK_KV8_I8, torch.float32)
 
 
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_attn_long_rows_without_queries(n_q):
+    """Rows that many teams share, some of them without a query: left as they were."""
+    lens = [9000, 4000, 20000, 700, 5000]
+    _check_attn(lens, 2, 4, n_q, 16, SPARK_KV8_E4M3, torch.bfloat16, n_new=[0, n_q, 0, 0, 1])
+    _check_attn(lens, 1, 13, n_q, 32, SPARK_KV8_I8, torch.float32, n_new=[0, n_q, 0, 0, 1])
+
+
 def test_attn_very_long():
     _check_attn([131072, 65537], 2, 4, 1, 32, SPARK_KV8_E4M3, torch.bfloat16)
 
