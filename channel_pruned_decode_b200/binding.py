@@ -421,7 +421,7 @@ class KV8Cache:
         desc = spark_kv8cache(self.n_pages, self.Hkv, self.page, self.D, self.type, _ptr(self.k), _ptr(self.v),
                               _ptr(self.k_scale), _ptr(self.v_scale))
         object.__setattr__(self, "_struct", desc)
-        object.__setattr__(self, "ref", ctypes.byref(desc))
+        object.__setattr__(self, "address", ctypes.addressof(desc))
         object.__setattr__(self, "index", self.k.get_device())
 
     @staticmethod
@@ -439,9 +439,8 @@ class KV8Cache:
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
     """The library sees bare pointers: a tensor of another type, shape, layout
-    or device than the call needs is refused here.  (The calls below first test
-    all their tensors in one expression, which costs a decode step's small calls
-    a quarter of a microsecond a tensor, and come here only to say what is wrong.)"""
+    or device than the call needs is refused.  (csrc/calls.cpp tests the calls'
+    tensors; where one does not fit, this says which and why.)"""
     if t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} needed, got {t.dtype}")
     if t.shape != shape:
@@ -452,19 +451,35 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
         raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {device}")
 
 
-def _need_ws(ws: torch.Tensor, device) -> None:
+def _refuse(where: str, ws: torch.Tensor, device, *tensors) -> None:
+    """A call whose tensors do not fit: say which (name, tensor, dtype, shape)."""
+    for name, t, dtype, shape in tensors:
+        _need(t, name, dtype, shape, device)
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws: must be contiguous and on {device}")
+    raise ValueError(f"{where}: tensors must be on the current CUDA device, whole numbers must fit 32 bits")
 
 
-def _launch_stream(index: int, stream) -> int | None:
-    """The stream to launch on; kernels start on the current device, so the
-    tensors (on device `index`) must be there."""
-    if index < 0 or index != torch._C._cuda_getDevice():
-        raise ValueError("tensors must be on the current CUDA device")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return _stream(stream)
+_calls = None
+
+
+def _native():
+    """The compiled half of the calls below (raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise RuntimeError("the compiled binding (_calls.so) is missing or does not fit this Python; build it with "
+                               "`python -m channel_pruned_decode_b200.build`") from e
+        _calls = m
+    return _calls
+
+
+def _raw(stream):
+    """A stream as the compiled calls take it: None for the current one."""
+    return stream if stream is None else _stream(stream)
 
 
 def spark_kv8_sizes(n_pages: int, Hkv: int, page: int, D: int = 128) -> tuple[int, list[int]]:
@@ -478,25 +493,13 @@ def spark_pages_extend(lens: torch.Tensor, n_new: torch.Tensor, page: int, pool:
                        ws: torch.Tensor, stream=None) -> None:
     """Pages for each row's n_new tokens (table [B, cap] and taken_out) and
     their slots [B, n_cap]; lens_out / taken_out may be lens / taken."""
-    i32, index, B = torch.int32, lens.get_device(), lens.numel()
-    (rows, cap), (rows_s, n_cap), n_pages = table.shape, slots.shape, pool.numel()
-    if not (lens.dtype is n_new.dtype is pool.dtype is taken.dtype is table.dtype is slots.dtype is lens_out.dtype
-            is taken_out.dtype is i32 and n_new.numel() == lens_out.numel() == rows == rows_s == B
-            and taken.numel() == taken_out.numel() == 1
-            and lens.is_contiguous() and n_new.is_contiguous() and pool.is_contiguous() and table.is_contiguous()
-            and slots.is_contiguous() and lens_out.is_contiguous()
-            and n_new.get_device() == pool.get_device() == taken.get_device() == table.get_device()
-            == slots.get_device() == lens_out.get_device() == taken_out.get_device() == ws.get_device() == index
-            and ws.is_contiguous()):
-        _need_ws(ws, lens.device)
-        for t, name, shape in ((lens, "lens", (B,)), (n_new, "n_new", (B,)), (pool, "pool", (n_pages,)),
-                               (taken, "taken", (1,)), (table, "table", (B, cap)), (slots, "slots", (B, n_cap)),
-                               (lens_out, "lens_out", (B,)), (taken_out, "taken_out", (1,))):
-            _need(t, name, i32, shape, lens.device)
-    rc = lib().spark_pages_extend(lens.data_ptr(), n_new.data_ptr(), B, page, pool.data_ptr(), n_pages,
-                                  taken.data_ptr(), table.data_ptr(), cap, n_cap, slots.data_ptr(),
-                                  lens_out.data_ptr(), taken_out.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                  _launch_stream(index, stream))
+    rc = _native().pages_extend(lens, n_new, page, pool, taken, table, slots, lens_out, taken_out, ws, _raw(stream))
+    if rc < 0:
+        i32, B = torch.int32, lens.shape[0]
+        _refuse("spark_pages_extend", ws, lens.device, ("lens", lens, i32, (B,)), ("n_new", n_new, i32, (B,)),
+                ("pool", pool, i32, (pool.numel(),)), ("taken", taken, i32, (1,)),
+                ("table", table, i32, (B, table.shape[-1])), ("slots", slots, i32, (B, slots.shape[-1])),
+                ("lens_out", lens_out, i32, (B,)), ("taken_out", taken_out, i32, (1,)))
     if rc:
         _check(rc, "spark_pages_extend")
 
@@ -506,23 +509,13 @@ def spark_pages_trim(lens: torch.Tensor, keep: torch.Tensor, page: int, pool: to
                      stream=None) -> None:
     """Cut each row to its first keep tokens and give the pages behind them
     back to the pool; lens_out / taken_out may be lens / taken."""
-    i32, index, B = torch.int32, lens.get_device(), lens.numel()
-    (rows, cap), n_pages = table.shape, pool.numel()
-    if not (lens.dtype is keep.dtype is pool.dtype is taken.dtype is table.dtype is lens_out.dtype
-            is taken_out.dtype is i32 and keep.numel() == lens_out.numel() == rows == B
-            and taken.numel() == taken_out.numel() == 1
-            and lens.is_contiguous() and keep.is_contiguous() and pool.is_contiguous() and table.is_contiguous()
-            and lens_out.is_contiguous()
-            and keep.get_device() == pool.get_device() == taken.get_device() == table.get_device()
-            == lens_out.get_device() == taken_out.get_device() == ws.get_device() == index and ws.is_contiguous()):
-        _need_ws(ws, lens.device)
-        for t, name, shape in ((lens, "lens", (B,)), (keep, "keep", (B,)), (pool, "pool", (n_pages,)),
-                               (taken, "taken", (1,)), (table, "table", (B, cap)), (lens_out, "lens_out", (B,)),
-                               (taken_out, "taken_out", (1,))):
-            _need(t, name, i32, shape, lens.device)
-    rc = lib().spark_pages_trim(lens.data_ptr(), keep.data_ptr(), B, page, pool.data_ptr(), n_pages,
-                                taken.data_ptr(), table.data_ptr(), cap, lens_out.data_ptr(), taken_out.data_ptr(),
-                                ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    rc = _native().pages_trim(lens, keep, page, pool, taken, table, lens_out, taken_out, ws, _raw(stream))
+    if rc < 0:
+        i32, B = torch.int32, lens.shape[0]
+        _refuse("spark_pages_trim", ws, lens.device, ("lens", lens, i32, (B,)), ("keep", keep, i32, (B,)),
+                ("pool", pool, i32, (pool.numel(),)), ("taken", taken, i32, (1,)),
+                ("table", table, i32, (B, table.shape[-1])), ("lens_out", lens_out, i32, (B,)),
+                ("taken_out", taken_out, i32, (1,)))
     if rc:
         _check(rc, "spark_pages_trim")
 
@@ -531,19 +524,13 @@ def spark_kv8_append(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tens
                      stream=None) -> None:
     """Write k_new, v_new [B, Hkv, n_cap, D] into the slots [B, n_cap] in 8
     bits ([B, Hkv, D] with n_cap = 1)."""
-    B, n_cap = slots.shape
-    index, dt = kc.index, k_new.dtype
-    shape = (B, kc.Hkv, kc.D) if n_cap == 1 and k_new.dim() == 3 else (B, kc.Hkv, n_cap, kc.D)
-    if not (k_new.shape == shape and v_new.shape == shape and v_new.dtype is dt and slots.dtype is torch.int32
-            and k_new.is_contiguous() and v_new.is_contiguous() and slots.is_contiguous()
-            and k_new.get_device() == v_new.get_device() == slots.get_device() == ws.get_device() == index
-            and ws.is_contiguous()):
-        _need_ws(ws, kc.k.device)
-        _need(k_new, "k_new", dt, shape, kc.k.device)
-        _need(v_new, "v_new", dt, shape, kc.k.device)
-        _need(slots, "slots", torch.int32, (B, n_cap), kc.k.device)
-    rc = lib().spark_kv8_append(k_new.data_ptr(), v_new.data_ptr(), B, n_cap, _dtype_code(dt), slots.data_ptr(),
-                                kc.ref, ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    rc = _native().kv8_append(k_new, v_new, slots, kc.address, kc.index, ws, _raw(stream))
+    if rc < 0:
+        B, n_cap = slots.shape
+        _dtype_code(k_new.dtype)
+        shape = (B, kc.Hkv, kc.D) if n_cap == 1 and k_new.dim() == 3 else (B, kc.Hkv, n_cap, kc.D)
+        _refuse("spark_kv8_append", ws, kc.k.device, ("k_new", k_new, k_new.dtype, shape),
+                ("v_new", v_new, k_new.dtype, shape), ("slots", slots, torch.int32, (B, n_cap)))
     if rc:
         _check(rc, "spark_kv8_append")
 
@@ -552,31 +539,14 @@ def spark_decode_attn_kv8(q: torch.Tensor, kc: KV8Cache, table: torch.Tensor, le
                           out: torch.Tensor, ws: torch.Tensor, n_new: torch.Tensor = None, stream=None) -> None:
     """Attention of q [B, Hkv*G, n_q, D] (or [B, Hkv*G, D]), each row's newest
     tokens, over its pages; out fp32, shaped like q."""
-    B, cap = table.shape
-    index, i32, dt = kc.index, torch.int32, q.dtype
-    if q.dim() == 4:
-        n_q = q.shape[2]
-        shape = (B, kc.Hkv * G, n_q, kc.D)
-    else:
-        n_q, shape = 1, (B, kc.Hkv * G, kc.D)
-    if not (q.shape == shape and out.shape == shape and out.dtype is torch.float32
-            and table.dtype is lens.dtype is i32 and lens.numel() == B
-            and q.is_contiguous() and out.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
-            and q.get_device() == out.get_device() == table.get_device() == lens.get_device() == ws.get_device() == index
-            and ws.is_contiguous()
-            and (n_new is None or (n_new.dtype is i32 and n_new.numel() == B and n_new.is_contiguous()
-                                   and n_new.get_device() == index))):
-        dev = kc.k.device
-        _need_ws(ws, dev)
-        _need(q, "q", dt, shape, dev)
-        _need(out, "out", torch.float32, shape, dev)
-        _need(table, "table", i32, (B, cap), dev)
-        _need(lens, "lens", i32, (B,), dev)
-        if n_new is not None:
-            _need(n_new, "n_new", i32, (B,), dev)
-    rc = lib().spark_decode_attn_kv8(q.data_ptr(), _dtype_code(dt), kc.ref, table.data_ptr(), cap, lens.data_ptr(),
-                                     None if n_new is None else n_new.data_ptr(), B, G, n_q, out.data_ptr(),
-                                     ws.data_ptr(), ws.nbytes, _launch_stream(index, stream))
+    rc = _native().decode_attn_kv8(q, kc.address, kc.index, table, lens, G, out, ws, n_new, _raw(stream))
+    if rc < 0:
+        i32, (B, cap) = torch.int32, table.shape
+        _dtype_code(q.dtype)
+        shape = (B, kc.Hkv * G, q.shape[2], kc.D) if q.dim() == 4 else (B, kc.Hkv * G, kc.D)
+        _refuse("spark_decode_attn_kv8", ws, kc.k.device, ("q", q, q.dtype, shape), ("out", out, torch.float32, shape),
+                ("table", table, i32, (B, cap)), ("lens", lens, i32, (B,)),
+                *([] if n_new is None else [("n_new", n_new, i32, (B,))]))
     if rc:
         _check(rc, "spark_decode_attn_kv8")
 

@@ -11,6 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspark.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["api.cu", "prune.cu", "decode.cu", "snapkv.cu", "think.cu", "pages.cu", "kv8.cu", "attn_kv8.cu"]
 NVCC_FLAGS = [
@@ -34,12 +35,36 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile csrc/calls.cpp, the native half of the binding of the paged
+    8-bit cache's calls, into _calls.so beside libspark.so."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "spark.h"), LIB]):
+        return CALLS
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [INCLUDE, sysconfig.get_path("include"), cuda, *include_paths()]
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for i in includes for x in ("-isystem", i)] + [src, "-o", CALLS + ".tmp"]
+    for d in library_paths():
+        cmd += ["-L", d]
+    cmd += ["-L", PKG, "-lspark", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ into libspark.so (exported: the C ABI of
     include/spark.h only).  Returns the library path."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, "spark_internal.cuh"), os.path.join(CSRC, "kv8.cuh"), os.path.join(INCLUDE, "spark.h")]
     if not force and not _stale(LIB, deps):
+        build_calls()
         return LIB
     nvcc = _nvcc()
     objdir = os.path.join(PKG, "_build")
@@ -57,6 +82,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run([nvcc, "-shared", "-cudart", "static", "-gencode", "arch=compute_100a,code=sm_100a",
                     "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    build_calls(force)
     return LIB
 
 
