@@ -194,11 +194,6 @@ __device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p) {
     return r;
 }
 
-// A kernel launched with programmatic serialisation may start before the one
-// ahead of it has ended; it touches no global memory before this wait.
-__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // A place on the line of steps.
 struct Place {
     int b, h, s;       // row, kv head, step of the row
@@ -217,7 +212,7 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ int clamped_len(const AttnArgs &a, int b) {
-    return min(max(__ldg(a.lens + b), 0), a.table_cap * a.kc.page);
+    return min(max(a.lens[b], 0), a.table_cap * a.kc.page);
 }
 
 __device__ __forceinline__ void set_row(const AttnArgs &a, Place &p, int b) {
@@ -255,11 +250,11 @@ __device__ __forceinline__ void load_batch(const AttnArgs &a, const Place &p, in
     t.ks = t.vs = 0.f;
     const int tok = p.s * kStep + lane * 16;
     if (tok < p.len && lane < 2 * n) {
-        const int pg = __ldg(a.table + (size_t)p.b * a.table_cap + (tok >> (31 - __clz(a.kc.page))));
+        const int pg = a.table[(size_t)p.b * a.table_cap + (tok >> (31 - __clz(a.kc.page)))];
         if ((unsigned)pg < (unsigned)a.kc.n_pages) {
             t.pg = pg;
-            t.ks = __ldg(a.kc.k_scale + (size_t)pg * a.kc.Hkv + p.h);
-            t.vs = __ldg(a.kc.v_scale + (size_t)pg * a.kc.Hkv + p.h);
+            t.ks = a.kc.k_scale[(size_t)pg * a.kc.Hkv + p.h];
+            t.vs = a.kc.v_scale[(size_t)pg * a.kc.Hkv + p.h];
         } else {
             *bad = true;
         }
@@ -307,7 +302,7 @@ __device__ __forceinline__ void write_row(float *out, const Merged &r) {
 template <typename E, int kType, int kNT>
 __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    const E *__restrict__ q, const AttnArgs a) {
+                    const E *q, const AttnArgs a) {
     constexpr int kAtWarps = AtGeom<kNT>::kWarps, kAtThreads = AtGeom<kNT>::kThreads;
     constexpr int kN = kNT ? kNT : 1;              // 8-row groups
     constexpr int kRows = kNT ? 8 * kNT : 4;       // query rows of a warp
@@ -348,7 +343,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     const int parts = max(1, kAtWarps / a.rows);  // of the last merge: warps per row
     const int mg_row = warp / parts, mg_part = warp - mg_row * parts;
     const int per = (a.B + kAtThreads - 1) / kAtThreads, n_look = (a.B + per - 1) / max(per, 1);  // rows a thread looks at
-    let_next_kernel_start();
     wait_for_prior_kernel();
 
     // ---- the line: steps before each thread's rows, and in all
@@ -359,8 +353,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
             if (b < a.B) {
-                const int len = clamped_len(a, b), nn = a.n_new ? __ldg(a.n_new + b) : a.n_q;
-                bad |= len != __ldg(a.lens + b) || nn < 0 || nn > a.n_q;
+                const int len = clamped_len(a, b), nn = a.n_new ? a.n_new[b] : a.n_q;
+                bad |= len != a.lens[b] || nn < 0 || nn > a.n_q;
                 mine += (len + kStep - 1) / kStep;
             }
         }
@@ -484,7 +478,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     auto begin_pair = [&](const StageMeta &mt) {
         b = mt.b;
         h = mt.h;
-        nn = opaque(a.n_new != nullptr) ? min(max(__ldg(a.n_new + b), 0), a.n_q) : a.n_q;
+        nn = opaque(a.n_new != nullptr) ? min(max(a.n_new[b], 0), a.n_q) : a.n_q;
         first_full = uniform(mt.len - nn + 1);  // tokens below this are seen by every query
         starts_pair = mt.s == 0;
         E_top = exp2_int(-100);
@@ -498,7 +492,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 const uint4 *src = reinterpret_cast<const uint4 *>(qb + (size_t)r * kD + c * 32);
 #pragma unroll
                 for (int i = 0; i < (int)sizeof(E) * 2; ++i) {
-                    const uint4 u = __ldg(src + i);
+                    const uint4 u = src[i];
                     const E *e = reinterpret_cast<const E *>(&u);
 #pragma unroll
                     for (int j = 0; j < 16 / (int)sizeof(E); ++j) x[i * (16 / (int)sizeof(E)) + j] = Elem<E>::to_f(e[j]);
@@ -879,7 +873,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll 1
     for (int r = blockIdx.x * kAtWarps + warp; r < a.B; r += gridDim.x * kAtWarps) {
         if (clamped_len(a, r) > 0) continue;
-        const int n = a.n_new ? min(max(__ldg(a.n_new + r), 0), a.n_q) : a.n_q;
+        const int n = a.n_new ? min(max(a.n_new[r], 0), a.n_q) : a.n_q;
         float4 *dst = reinterpret_cast<float4 *>(a.out + (size_t)r * Hkv * a.rows * kD);
 #pragma unroll 1
         for (int i = 0; i < Hkv * a.rows; ++i)
@@ -1057,17 +1051,8 @@ static cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, cons
     auto kernel = attn_kv8_kernel<E, kType, kNT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)num_sms);
-    cfg.blockDim = dim3(AtGeom<kNT>::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, mk, mv, static_cast<const E *>(q), a);
+    return launch_after_prior(kernel, (unsigned)num_sms, AtGeom<kNT>::kThreads, smem, st, mk, mv,
+                              static_cast<const E *>(q), a);
 }
 
 template <typename E, int kType>

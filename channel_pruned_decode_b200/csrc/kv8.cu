@@ -167,8 +167,8 @@ template <int kType> __device__ __forceinline__ uint32_t encode4(const float (&f
 // hidden by 32 warps with 4 KB under way each, not inside one.
 template <typename E, int kType>
 __global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps)
-    kv8_append_kernel(const E *__restrict__ k_new, const E *__restrict__ v_new, int B, int n_cap,
-                      const int32_t *__restrict__ slots, spark_kv8cache kc, int pieces, int per, uint32_t *status) {
+    kv8_append_kernel(const E *k_new, const E *v_new, int B, int n_cap, const int32_t *slots,
+                      spark_kv8cache kc, int pieces, int per, uint32_t *status) {
     constexpr int kWarps = ApGeom<E>::kWarps, kTokens = ApGeom<E>::kTokens;
     __shared__ float part[kWarps];
     constexpr int kVec = 16 / (int)sizeof(E);       // values per 16-byte load
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(ApGeom<E>::kWarps * 32, 32 / ApGeom<E>::kWarps
     const int last = min(first + per, 2 * Hkv);
     const int32_t *row = slots + (size_t)b * n_cap;
     const int n_slots = kc.n_pages * page;
+    wait_for_prior_kernel();
     // a piece is what falls into one page if the row's slots follow one another
     const int o0 = max(row[0], 0) & (page - 1);
     const int begin = max(0, piece * page - o0), end = min(n_cap, (piece + 1) * page - o0);
@@ -299,13 +300,8 @@ static cudaError_t launch_append(const E *k_new, const E *v_new, int B, int n_ca
     const long units = (long)B * pieces * ((2 * kc.Hkv + per - 1) / per);
     const unsigned grid = (unsigned)((units + teams - 1) / teams);
     uint32_t *status = static_cast<uint32_t *>(ws);
-    if (kc.type == SPARK_KV8_E4M3)
-        kv8_append_kernel<E, SPARK_KV8_E4M3><<<grid, kWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc, pieces,
-                                                                           per, status);
-    else
-        kv8_append_kernel<E, SPARK_KV8_I8><<<grid, kWarps * 32, 0, st>>>(k_new, v_new, B, n_cap, slots, kc, pieces, per,
-                                                                         status);
-    return cudaGetLastError();
+    auto kernel = kc.type == SPARK_KV8_E4M3 ? kv8_append_kernel<E, SPARK_KV8_E4M3> : kv8_append_kernel<E, SPARK_KV8_I8>;
+    return launch_after_prior(kernel, grid, kWarps * 32, 0, st, k_new, v_new, B, n_cap, slots, kc, pieces, per, status);
 }
 
 cudaError_t launch_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int dtype,

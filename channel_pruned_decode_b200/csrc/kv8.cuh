@@ -51,4 +51,32 @@ template <int kType> __device__ __forceinline__ __half2 kv8_decode2(uint32_t two
     return __floats2half2_rn((float)(int8_t)(two & 0xff), (float)(int8_t)((two >> 8) & 0xff));
 }
 
+// ---------------------------------------------------- programmatic launches
+// The calls of a serving step follow one another on a stream, and the smaller
+// ones take less time than a launch.  These kernels are launched so that one may
+// be set up while the one ahead of it ends; each touches no global memory before
+// wait_for_prior_kernel().  What it then reads may have been written while it was
+// already resident, so such data is read with plain loads, never as read-only
+// (no __ldg, no const __restrict__).
+__device__ __forceinline__ void wait_for_prior_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... K, typename... A>
+inline cudaError_t launch_after_prior(void (*kernel)(K...), unsigned grid, unsigned block, size_t smem,
+                                      cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+}
+
 }  // namespace spark

@@ -17,7 +17,7 @@
 // Bound by latency: a launch, the lengths, the pages (three dependent reads),
 // 4.1 us a call back to back for 64 rows (as much as the host takes) and 6.2 us
 // for 2 M slots (9 MB, 1.4 us at the copy rate).
-#include "spark_internal.cuh"
+#include "kv8.cuh"
 
 namespace spark {
 
@@ -94,15 +94,16 @@ __device__ __forceinline__ bool last_cta(uint32_t *ticket, int *flag) {
 }
 
 __global__ void __launch_bounds__(kPgThreads)
-    pages_extend_kernel(const int32_t *lens, const int32_t *__restrict__ n_new, int B, int shift,
-                        const int32_t *__restrict__ pool, int n_pages, const int32_t *taken, int32_t *table,
-                        int table_cap, int n_cap, int32_t *__restrict__ slots, int32_t *lens_out,
+    pages_extend_kernel(const int32_t *lens, const int32_t *n_new, int B, int shift,
+                        const int32_t *pool, int n_pages, const int32_t *taken, int32_t *table,
+                        int table_cap, int n_cap, int32_t *slots, int32_t *lens_out,
                         int32_t *taken_out, int chunks, int in_place, uint32_t *ws) {
     __shared__ int sm[kPgThreads / 32];
     __shared__ int flag;
     const int b = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     const int tid = threadIdx.x;
     const int max_len = table_cap << shift;
+    wait_for_prior_kernel();
     const int tk = min(max(*taken, 0), n_pages);
     int before = 0;
     for (int i = tid; i < b; i += kPgThreads) {
@@ -179,13 +180,14 @@ __global__ void __launch_bounds__(kPgThreads)
 }
 
 __global__ void __launch_bounds__(kPgThreads)
-    pages_trim_kernel(const int32_t *lens, const int32_t *__restrict__ keep, int B, int shift, int32_t *pool,
-                      int n_pages, const int32_t *taken, const int32_t *__restrict__ table, int table_cap,
+    pages_trim_kernel(const int32_t *lens, const int32_t *keep, int B, int shift, int32_t *pool,
+                      int n_pages, const int32_t *taken, const int32_t *table, int table_cap,
                       int32_t *lens_out, int32_t *taken_out, int in_place, uint32_t *ws) {
     __shared__ int sm[kPgThreads / 32];
     __shared__ int flag;
     const int b = blockIdx.x, tid = threadIdx.x;
     const int max_len = table_cap << shift;
+    wait_for_prior_kernel();
     const int tk = min(max(*taken, 0), n_pages);
     // len and kept tokens of a row, in range
     auto row_of = [&](int i, bool *bad) {
@@ -233,19 +235,18 @@ cudaError_t launch_pages_extend(const int32_t *lens, const int32_t *n_new, int B
                                 int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
                                 int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *ws, cudaStream_t st) {
     const int chunks = n_cap > kPgSlots ? (n_cap + kPgSlots - 1) / kPgSlots : 1;
-    pages_extend_kernel<<<(unsigned)((long)B * chunks), kPgThreads, 0, st>>>(
-        lens, n_new, B, log2_page(page), pool, n_pages, taken, table, table_cap, n_cap, slots, lens_out, taken_out,
-        chunks, lens_out == lens || taken_out == taken, static_cast<uint32_t *>(ws));
-    return cudaGetLastError();
+    return launch_after_prior(pages_extend_kernel, (unsigned)((long)B * chunks), kPgThreads, 0, st, lens, n_new, B,
+                              log2_page(page), pool, n_pages, taken, table, table_cap, n_cap, slots, lens_out,
+                              taken_out, chunks, (int)(lens_out == lens || taken_out == taken),
+                              static_cast<uint32_t *>(ws));
 }
 
 cudaError_t launch_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool, int n_pages,
                               const int32_t *taken, const int32_t *table, int table_cap, int32_t *lens_out,
                               int32_t *taken_out, void *ws, cudaStream_t st) {
-    pages_trim_kernel<<<(unsigned)B, kPgThreads, 0, st>>>(
-        lens, keep, B, log2_page(page), pool, n_pages, taken, table, table_cap, lens_out, taken_out,
-        lens_out == lens || taken_out == taken, static_cast<uint32_t *>(ws));
-    return cudaGetLastError();
+    return launch_after_prior(pages_trim_kernel, (unsigned)B, kPgThreads, 0, st, lens, keep, B, log2_page(page), pool,
+                              n_pages, taken, table, table_cap, lens_out, taken_out,
+                              (int)(lens_out == lens || taken_out == taken), static_cast<uint32_t *>(ws));
 }
 
 }  // namespace spark
