@@ -37,7 +37,7 @@
 // stage's arrival and the last step), with 2.6 us before it (lengths, their
 // sum, table, pages: four dependent reads) and 4 to 8 us behind it (slowest
 // SM, merges).  At 16 rows by dependent-issue latency: 255 registers leave 8
-// warps, issue slots are 35 % used, and 78 us of 4 verified tokens compare
+// warps, issue slots are 35 % used, and 75 to 77 us of 4 verified tokens compare
 // with 41 us of memory time.
 #include <cuda.h>  // CUtensorMap and its enums (the encoder is fetched at run time)
 

@@ -1,7 +1,7 @@
 // Native half of the Python binding of the paged 8-bit cache's calls: checks
 // the tensors and calls the C ABI.  A decode step makes three of these calls a
 // layer, and their checks and argument conversion in Python cost more than the
-// kernels of a small step (7.5 us a call, against 4 here).
+// kernels of a small step (7.5 us a call; here less than the launch).
 //
 // Each function takes the Python function's arguments in order, then the
 // stream (None: the current one), and returns the library's status, or -1

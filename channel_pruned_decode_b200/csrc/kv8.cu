@@ -7,7 +7,8 @@
 // of the rows (up to `page` tokens of one head, 4 KB a warp in bf16) stays in
 // registers between the maximum and the conversion.  Bound by memory: each
 // value is read once and its code written once (32 rows of 2048 tokens, 8 heads
-// in bf16: 65 to 67 us for 378 MB, 87 % of the copy rate; issue slots 60 % used).
+// in bf16: 63 to 66 us for 378 MB, 88 to 92 % of the copy rate; issue slots
+// 60 % used).
 #include "kv8.cuh"
 
 namespace spark {
@@ -292,9 +293,11 @@ static cudaError_t launch_append(const E *k_new, const E *v_new, int B, int n_ca
     const int pieces = (n_cap + kc.page - 2) / kc.page + 1;  // a row may start on a page's last place
     const int teams = kWarps / (kc.page / ApGeom<E>::kTokens);
     // Where the GPU is full more than once, a team takes the keys and the values
-    // of a head, which share its look at the slots.  32 x 2048 tokens of 8 heads
-    // in bf16: 1 at a time 77.7 us, 2 70.1, 4 71.4, 8 75.4, 16 77.0; 5 x 1777
-    // tokens of 4 heads in fp32: 14.4, 13.6, 16.1, 24.6 (the GPU no longer full).
+    // of a head, which share its look at the slots.  32 x
+    // 2048 tokens of 8 heads in bf16: 1 at a time 77.7 us, 2 70.1, 4 71.4, 8 75.4,
+    // 16 77.0; 5 x 1777 tokens of 4 heads in fp32: 14.4, 13.6, 16.1, 24.6 (the GPU
+    // no longer full).  That was before later steps: 2 at a time now takes 63 to
+    // 66 us and 10.4, the others were not measured again.
     const long warps = (long)B * pieces * kc.Hkv * 2 * (kWarps / teams);
     const int per = warps > 32l * num_sms ? 2 : 1;
     const long units = (long)B * pieces * ((2 * kc.Hkv + per - 1) / per);

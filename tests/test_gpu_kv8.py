@@ -541,6 +541,37 @@ def test_step_replayed_from_a_graph():
     del g
 
 
+@pytest.mark.parametrize("B,H,G,n", [(3, 2, 4, 1), (8, 8, 4, 3), (1, 8, 4, 4)])
+def test_steps_behind_one_another(B, H, G, n):
+    """Steps without anything between them (each kernel is set up while the one
+    ahead of it ends) give what the same steps give when each call is waited for."""
+    rng = random.Random(B)
+    steps = 40
+    ins = [_inputs(400 + i, B, H, G, n, torch.bfloat16) for i in range(steps)]
+    nn = [i32([rng.randint(0, n) for _ in range(B)]) for _ in range(steps)]
+    keep = [i32([rng.choice([10 ** 6, 10 ** 6, rng.randint(0, 60)]) for _ in range(B)]) for _ in range(steps)]
+    fast, slow = (_Serve(B, H, G, 16, SPARK_KV8_E4M3, 400, 40, n, torch.bfloat16) for _ in range(2))
+    torch.cuda.synchronize()
+    for i in range(steps):
+        fast.step(nn[i], *ins[i])
+        fast.trim(keep[i])
+    torch.cuda.synchronize()
+    for i in range(steps):
+        k, v, q = ins[i]
+        spark_pages_extend(slow.lens, nn[i], 16, slow.pool, slow.taken, slow.table, slow.slots, slow.lens, slow.taken,
+                           slow.ws)
+        torch.cuda.synchronize()
+        spark_kv8_append(k, v, slow.slots, slow.kc, slow.ws)
+        torch.cuda.synchronize()
+        spark_decode_attn_kv8(q, slow.kc, slow.table, slow.lens, G, slow.out, slow.wsa, n_new=nn[i])
+        torch.cuda.synchronize()
+        slow.trim(keep[i])
+        torch.cuda.synchronize()
+    for name in ("out", "lens", "taken", "pool", "slots"):
+        assert torch.equal(getattr(fast, name), getattr(slow, name)), name
+    assert fast.status() == slow.status() == (0, 0)
+
+
 def test_two_streams_with_workspaces_of_their_own():
     """Two serving loops on two streams at once do not disturb each other."""
     shape = (5, 4, 4, 16, SPARK_KV8_I8, 100, 8, 4, torch.bfloat16)
