@@ -169,3 +169,18 @@ def test_oracle_page_pins():
     assert out and taken == 1 and lens == [32] and slots[0][17:] == [-1] * 3
     pool, lens, taken = R.trim([17, 40], [16, 0], 16, [0, 1, 2, 3, 4, 5], 5, [[8, 9, -1], [10, 11, 12]])
     assert pool == [0, 9, 10, 11, 12, 5] and lens == [16, 0] and taken == 1
+
+
+def _extend(L, b=1, page=16, n_pages=8, cap=4, n=4):
+    return L.spark_pages_extend(16, 32, b, page, 16, n_pages, 16, 16, cap, n, 16, 48, 64, 256, 256, None)
+
+
+def _trim(L, b=1, page=16, n_pages=8, cap=4):
+    return L.spark_pages_trim(16, 32, b, page, 16, n_pages, 16, 16, cap, 48, 64, 256, 256, None)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_pool_beyond_32_bit_slots(L, page):
+    """A slot is page number * page + place in 32 bits."""
+    n = (1 << 31) // page
+    assert _extend(L, page=page, n_pages=n) == _trim(L, page=page, n_pages=n) == B.SPARK_ERR_UNSUPPORTED
