@@ -446,7 +446,8 @@ int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int pag
     const int rc = check_pages(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, lens_out, taken_out);
     if (rc != SPARK_OK) return rc;
     if (n_cap < 0) return SPARK_ERR_ARG;
-    if ((double)B * (n_cap / 2048 + 1) > 2147483647.0) return SPARK_ERR_UNSUPPORTED;  // CTAs
+    // CTAs; and a place in a row of slots plus a CTA's stride stays in 32 bits
+    if ((double)B * (n_cap / 2048 + 1) > 2147483647.0 || n_cap > (1 << 30)) return SPARK_ERR_UNSUPPORTED;
     if (B == 0) return SPARK_OK;
     if (n_cap > 0 && (!slots || !aligned16(slots))) return SPARK_ERR_ARG;
     if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;

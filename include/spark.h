@@ -493,7 +493,7 @@ SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t s
  * pages hold, taken outside [0, n_pages], a page number outside the pool)
  * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
  * Requires B * table_cap + n_pages < 2^31, table_cap * page < 2^31 and
- * n_pages * page < 2^31.
+ * n_pages * page < 2^31, and n_cap <= 2^30.
  * Workspace: 256 bytes, all zero before first use, not shared with a call
  * that may run at the same time (this holds for every workspace of the library).
  * B = 0 launches nothing and leaves taken_out as it is.

@@ -184,3 +184,7 @@ def test_pool_beyond_32_bit_slots(L, page):
     """A slot is page number * page + place in 32 bits."""
     n = (1 << 31) // page
     assert _extend(L, page=page, n_pages=n) == _trim(L, page=page, n_pages=n) == B.SPARK_ERR_UNSUPPORTED
+
+
+def test_more_new_tokens_than_a_row_can_index(L):
+    assert _extend(L, n=(1 << 30) + 1) == _extend(L, n=(1 << 31) - 1) == B.SPARK_ERR_UNSUPPORTED
