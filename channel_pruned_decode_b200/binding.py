@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of pruning and decode runs in the CUDA
 kernels of libspark.so.  The paged cache's calls, of which a decode step makes
-several a layer, are marshalled by csrc/calls.cpp.  torch tensors supply device memory and streams.
+several a layer, are marshalled by csrc/calls.cpp.  torch tensors supply device
+memory and streams.
 There is no CPU fallback: loading fails loudly when the library is missing.
 """
 from __future__ import annotations

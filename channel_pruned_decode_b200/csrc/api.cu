@@ -427,7 +427,8 @@ static int check_pages(const int32_t *lens, const int32_t *n, int B, int page, c
     if (B < 0 || n_pages < 0 || table_cap < 0) return SPARK_ERR_ARG;
     if (!kv8_page_ok(page)) return SPARK_ERR_UNSUPPORTED;
     if ((double)B * table_cap + n_pages > 2147483647.0 || (double)table_cap * page > 2147483647.0 ||
-        (double)n_pages * page > 2147483647.0)  // slots are int32
+        (double)n_pages * page > 2147483647.0 ||  // slots are int32
+        B > 65536)  // each CTA sums the rows before its own: work grows with B^2
         return SPARK_ERR_UNSUPPORTED;
     if (B == 0) return SPARK_OK;
     if (!lens || !n || !taken || !lens_out || !taken_out || (n_pages > 0 && !pool) || (table_cap > 0 && !table))

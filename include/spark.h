@@ -493,7 +493,7 @@ SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t s
  * pages hold, taken outside [0, n_pages], a page number outside the pool)
  * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
  * Requires B * table_cap + n_pages < 2^31, table_cap * page < 2^31 and
- * n_pages * page < 2^31, and n_cap <= 2^30.
+ * n_pages * page < 2^31, n_cap <= 2^30 and B <= 65536.
  * Workspace: 256 bytes, all zero before first use, not shared with a call
  * that may run at the same time (this holds for every workspace of the library).
  * B = 0 launches nothing and leaves taken_out as it is.
@@ -578,8 +578,8 @@ SPARK_API size_t spark_workspace_bytes_kv8(int B, int Hkv, int G, int n_q);
 /* Synchronise `stream`, read the device status word at the start of
  * `workspace` into *status (SPARK_OK, SPARK_ERR_TIMEOUT when a bounded wait
  * ran out, SPARK_ERR_PAGES when a page pool ran out, SPARK_ERR_ARG when a
- * device-side length, budget, slot or page number was out of range) and, when clear != 0, reset it to zero.  Returns SPARK_ERR_CUDA if
- * a copy fails. */
+ * device-side length, budget, slot or page number was out of range) and, when
+ * clear != 0, reset it to zero.  Returns SPARK_ERR_CUDA if a copy fails. */
 SPARK_API int spark_device_status(void *workspace, int *status, int clear, void *stream);
 
 /*

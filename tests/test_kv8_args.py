@@ -188,3 +188,9 @@ def test_pool_beyond_32_bit_slots(L, page):
 
 def test_more_new_tokens_than_a_row_can_index(L):
     assert _extend(L, n=(1 << 30) + 1) == _extend(L, n=(1 << 31) - 1) == B.SPARK_ERR_UNSUPPORTED
+
+
+def test_more_rows_than_the_sums_are_made_for(L):
+    """Each CTA sums the rows before its own, so work grows with the square."""
+    b = (1 << 16) + 1
+    assert _extend(L, b=b) == _trim(L, b=b) == _trim(L, b=(1 << 31) - 1, cap=0) == B.SPARK_ERR_UNSUPPORTED
