@@ -10,7 +10,9 @@
 //           behind it go back to pool[taken - total + (pages of rows before)].
 // Both are a prefix sum over the rows and a copy.  Each CTA sums the rows
 // before its own itself (a few loads a thread, from L2), which costs less than
-// a second launch for the sum.  lens_out may be lens and taken_out may be
+// a second launch for the sum at serving batches; the work grows with B^2 (one
+// token a row: 4 us for 512 rows, 13 for 4096, 95 for 16384, 1.2 ms for 65536, the
+// most a call takes; trim 3, 14, 162, 2.4 ms).  lens_out may be lens and taken_out may be
 // taken (a replayed graph advances them in place): they are then written by
 // the last CTA to finish, when every other one has read them.
 //

@@ -149,3 +149,29 @@ def test_pages_come_back_in_the_order_they_are_taken():
         assert spark_device_status(ws) == 0
         held = [p for row, x in zip(T.tolist(), L.tolist()) for p in row[:R.ceil_div(x, page)]]
         assert sorted(held + Pl.tolist()[tk.item():]) == list(range(n_pages))
+
+
+def test_largest_batch():
+    """65536 rows, the most a call takes: extended in place, then cut back to what they were."""
+    B, page, cap = 1 << 16, 16, 4
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 40, (B,), generator=g)
+    new = torch.randint(0, 3, (B,), generator=g)
+    have, want = (lens + page - 1) // page, (lens + new + page - 1) // page
+    ids = torch.randperm(int(want.sum()), generator=g)
+    held, places = int(have.sum()), torch.arange(cap)[None]
+    table = torch.full((B, cap), -9)
+    table[places < have[:, None]] = ids[:held]
+    full = table.clone()
+    full[(places >= have[:, None]) & (places < want[:, None])] = ids[held:]
+    at = lens[:, None] + torch.arange(2)[None]
+    slots = torch.gather(full, 1, (at // page).clamp(max=cap - 1)) * page + at % page
+    slots[torch.arange(2)[None] >= new[:, None]] = -1
+    put = lambda t: t.to(torch.int32).to(DEV)
+    L, N, T, P, K = put(lens), put(new), put(table), put(ids), put(lens)
+    tk, S, ws = i32([held]), put(torch.full((B, 2), -77)), workspace(256)
+    spark_pages_extend(L, N, page, P, tk, T, S, L, tk, ws)
+    assert torch.equal(L, put(lens + new)) and torch.equal(T, put(full)) and torch.equal(S, put(slots))
+    assert int(tk) == ids.numel() and spark_device_status(ws) == 0
+    spark_pages_trim(L, K, page, P, tk, T, L, tk, ws)
+    assert torch.equal(L, K) and torch.equal(P, put(ids)) and int(tk) == held and spark_device_status(ws) == 0
