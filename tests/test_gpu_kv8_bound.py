@@ -1,0 +1,87 @@
+"""Attention over the paged 8-bit cache held to the bound of
+tests/_kv8_bound.py, which is relative to sum p |v| of each channel."""
+import random
+
+import pytest
+import torch
+
+from channel_pruned_decode_b200 import (KV8Cache, spark_decode_attn_kv8, spark_device_status, spark_kv8_append,
+                                        spark_workspace_bytes_kv8, workspace, SPARK_KV8_E4M3, SPARK_KV8_I8)
+from tests import _kv8 as R
+from tests import _kv8_bound as A
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+D = 128
+KINDS = [SPARK_KV8_E4M3, SPARK_KV8_I8]
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _values(gen, shape, spread=0.5):
+    x = torch.randn(shape, generator=gen, device=DEV)
+    return x * torch.exp(spread * torch.randn(shape[:-2] + (1, D), generator=gen, device=DEV))
+
+
+def _cache(lens, H, page, kind, seed, mean=0.0):
+    """Rows of lens tokens in shuffled pages; values with the given mean."""
+    need = [R.ceil_div(x, page) for x in lens]
+    ids = list(range(sum(need)))
+    random.Random(seed).shuffle(ids)
+    kc = KV8Cache.empty(len(ids), H, page, kind)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device=DEV)
+    ws, g, at = workspace(256), _gen(seed), 0
+    for b, (x, n) in enumerate(zip(lens, need)):
+        table[b, :n] = i32(ids[at:at + n])
+        at += n
+        t = torch.arange(x, device=DEV)
+        slots = (table[b, t // page].long() * page + t % page).int()[None].contiguous()
+        k, v = (_values(g, (1, H, x, D)) for _ in range(2))
+        spark_kv8_append(k, v + mean, slots, kc, ws)
+    assert spark_device_status(ws) == 0
+    return kc, table
+
+
+def _worst(q, kc, table, lens, G, n_new=None, status=0):
+    B, Hq, n_q, _ = q.shape
+    out = torch.full(q.shape, float("nan"), dtype=torch.float32, device=DEV)
+    ws = workspace(spark_workspace_bytes_kv8(B, Hq // G, G, n_q))
+    spark_decode_attn_kv8(q, kc, table, i32(lens), G, out, ws, n_new=None if n_new is None else i32(n_new))
+    assert spark_device_status(ws) == status
+    nn = [n_q] * B if n_new is None else n_new
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ref, tol = A.attention(q, kc.k, kc.v, kc.k_scale, kc.v_scale, kc.type, table, lens, nn, G, kc.page, sms)
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    return A.worst(out, ref, tol)
+
+
+@pytest.mark.parametrize("mean", [0.0, 1.0])
+@pytest.mark.parametrize("lens,H,G,n_q,page,kind,dtype", [
+    ([131072, 65537], 2, 4, 1, 32, SPARK_KV8_E4M3, torch.bfloat16),
+    ([131072], 8, 4, 1, 16, SPARK_KV8_I8, torch.float32),
+    ([150000, 150001, 7], 8, 2, 1, 128, SPARK_KV8_I8, torch.bfloat16),
+    ([150000, 150001, 7], 8, 8, 1, 128, SPARK_KV8_E4M3, torch.bfloat16),
+    ([150000, 150001, 7], 8, 8, 2, 128, SPARK_KV8_I8, torch.bfloat16),
+    ([150000, 150001, 7], 8, 16, 2, 128, SPARK_KV8_E4M3, torch.bfloat16),
+    ([20011, 20012], 8, 8, 8, 64, SPARK_KV8_E4M3, torch.float32),
+    ([20011, 30000], 4, 13, 4, 32, SPARK_KV8_I8, torch.bfloat16)])
+def test_long_rows(lens, H, G, n_q, page, kind, dtype, mean):
+    kc, table = _cache(lens, H, page, kind, 3, mean)
+    q = _values(_gen(4), (len(lens), H * G, n_q, D)).to(dtype)
+    assert _worst(q, kc, table, lens, G) <= 1
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G,n_q,page", [(1, 1, 16), (4, 1, 32), (8, 1, 64), (4, 4, 16), (16, 2, 128), (8, 8, 16)])
+def test_short_rows(kind, dtype, G, n_q, page):
+    lens = [n_q, 15 + n_q, 100, 515, 2049]
+    kc, table = _cache(lens, 2, page, kind, 5)
+    q = _values(_gen(6), (len(lens), 2 * G, n_q, D)).to(dtype)
+    assert _worst(q, kc, table, lens, G) <= 1
