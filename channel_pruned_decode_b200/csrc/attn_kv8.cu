@@ -15,10 +15,11 @@
 // probabilities, so codes are only converted, never scaled.  A query row is
 // brought to [2^13, 2^14) by a power of two: bf16 is then exact in fp16
 // (elements 2^-27 below the row's largest lose bits), fp32 goes in as two
-// fp16 halves.  P is multiplied by 2^6 and by the page's value scale over a
-// power of two above every scale seen so far, and enters as two fp16 halves
-// (22 bits, down to 2^-31 of the largest weight), so the result is that of
-// fp32 arithmetic.  The codes of values are paired by token with byte permutes
+// fp16 halves (22 bits).  P is multiplied by the page's value scale and 2^6
+// over a power of two that follows the row's largest product of the two, and
+// enters as two fp16 halves: 22 bits, down to 2^-29 of that product, however
+// far the value scales of a row lie apart (up to 2^110).  The sums come out with
+// the error of fp32 ones.  The codes of values are paired by token with byte permutes
 // in registers (the transpose that the second product needs), P is transposed
 // by movmatrix; nothing else crosses lanes but the row maxima.
 //
@@ -60,8 +61,10 @@ constexpr int kStageBytes = 2 * kStep * kD;
 constexpr int kMaxStages = 24;             // stages of a CTA: 192 KB
 constexpr int kRingBytes = kMaxStages * kStageBytes;
 constexpr int kMinCtaSteps = 4;            // a CTA takes at least this many steps
-constexpr int kPScale = 6;                 // probabilities enter the second product times 2^6
-constexpr float kSlack = 8.f;              // log2 of how far a probability may pass its reference
+constexpr int kPScale = 6;                 // the row's largest p * value scale enters the second product near 2^6
+constexpr float kSlack = 5.f;              // log2 of how far a probability may pass its reference
+constexpr float kTopFactor = 1024.f;       // value scale * 2^6 / E up to which p <= 2^kSlack stays in fp16
+constexpr int kMinE = -120, kMaxE = 126;   // 2^(6 - E) and 2^(E - 6) are normal fp32
 
 // What a stage's consumers need to know beside the codes.
 struct __align__(16) StageMeta {
@@ -158,6 +161,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// 1 / x for a power of two; 2^127 for 0 (it then multiplies zeros).
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -472,7 +478,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     float qf[kN][2];              // score factor of rows 2c, 2c + 1
     int lim[kN][2];               // the last token they see
     float o[kN][8][4], m[kN][2], l[kN][2];
-    float E_top = 1.f, E_inv = 1.f;
+    float vs_max = 0.f;           // value scales up to this leave every p <= 2^kSlack in fp16
+    float pf[kN][2];              // 2^(6 - E), E: log2 of the row's largest p * value scale; 0: none yet
     int b = -1, h = 0, nn = 0, first_full = 0;
     bool starts_pair = false, ends_pair = false;
     auto begin_pair = [&](const StageMeta &mt) {
@@ -481,8 +488,6 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         nn = opaque(a.n_new != nullptr) ? min(max(a.n_new[b], 0), a.n_q) : a.n_q;
         first_full = uniform(mt.len - nn + 1);  // tokens below this are seen by every query
         starts_pair = mt.s == 0;
-        E_top = exp2_int(-100);
-        E_inv = exp2_int(100 + kPScale);
         const E *qb = q + ((size_t)b * Hkv + h) * a.rows * kD;
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
@@ -523,8 +528,9 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 qf[t][j] = __shfl_sync(0xffffffffu, mine, (2 * c + j) * 4);
                 lim[t][j] = qi[t][j] < nn ? mt.len - nn + qi[t][j] : -1;
                 m[t][j] = -INFINITY;
-                l[t][j] = 0.f;
+                l[t][j] = pf[t][j] = 0.f;
             }
+            vs_max = INFINITY;
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
         }
@@ -549,17 +555,18 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     const float k1 = was.y == -INFINITY ? 0.f : exp2_approx(was.y - m[t][1]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        o[t][j][0] += v[j].x * k0 * E_inv;
-                        o[t][j][1] += v[j].y * k1 * E_inv;
-                        o[t][j][2] += v[j].z * k0 * E_inv;
-                        o[t][j][3] += v[j].w * k1 * E_inv;
+                        o[t][j][0] += v[j].x * k0 * pf[t][0];
+                        o[t][j][1] += v[j].y * k1 * pf[t][1];
+                        o[t][j][2] += v[j].z * k0 * pf[t][0];
+                        o[t][j][3] += v[j].w * k1 * pf[t][1];
                     }
                 }
                 if (on_the_way) {
-                    const float f = E_top * exp2_int(-kPScale);
+                    const float f0 = inverse_pow2(pf[t][0]), f1 = inverse_pow2(pf[t][1]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        __stcg(mine + j * 32, make_float4(o[t][j][0] * f, o[t][j][1] * f, o[t][j][2] * f, o[t][j][3] * f));
+                        __stcg(mine + j * 32,
+                               make_float4(o[t][j][0] * f0, o[t][j][1] * f1, o[t][j][2] * f0, o[t][j][3] * f1));
                         o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
                     }
                     __stcg(mine + 8 * 32, make_float4(m[t][0], m[t][1], 0.f, 0.f));
@@ -596,10 +603,11 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                 const int row = wt * kRows + col;
                 if ((kNT == 0 && c >= 2) || qi[t][j] >= nn) continue;
                 float *dst;
-                float f = E_top * exp2_int(-kPScale);
+                const float f = inverse_pow2(pf[t][j]);
+                float f_l = 1.f;
                 if (whole) {
                     dst = a.out + (bh * a.rows + row) * kD;
-                    f = l[t][j] == 0.f ? 0.f : f / l[t][j];
+                    f_l = l[t][j] == 0.f ? 0.f : 1.f / l[t][j];
                 } else {
                     const size_t at = last ? (size_t)row : (size_t)(tm + bh) * a.rows + row;
                     dst = (last ? part : a.acc) + at * kD;
@@ -609,8 +617,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<float4 *>(dst + g * 16 + i * 4) =
-                        make_float4(o[t][2 * i][j] * f, o[t][2 * i][2 + j] * f, o[t][2 * i + 1][j] * f,
-                                    o[t][2 * i + 1][2 + j] * f);
+                        make_float4(o[t][2 * i][j] * f_l * f, o[t][2 * i][2 + j] * f_l * f,
+                                    o[t][2 * i + 1][j] * f_l * f, o[t][2 * i + 1][2 + j] * f_l * f);
             }
         }
     };
@@ -729,10 +737,12 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     }
                 }
             }
-            // The reference m of a row's probabilities (in units of log2) is its
-            // largest score so far, but follows it only when that is more than
-            // kSlack above: the sums take any reference, and most steps then
-            // need no maximum across lanes and no rescaling.
+            // The reference m of a row's probabilities (a power of two: its log2) is
+            // its largest score so far, rounded up, but follows it only when that is
+            // more than kSlack above: the sums take any reference, and most steps then
+            // need no maximum across lanes and no rescaling.  The same holds for E, the
+            // reference of the products p * value scale: it is looked at where m moves,
+            // and where a page's value scale alone might bring p out of fp16's range.
             float f[kN][2][2];
             bool move = false;
 #pragma unroll
@@ -746,30 +756,35 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                                            fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
                     move |= mx > m[t][j] + kSlack;
                 }
-            const float vm = fmaxf(mt.vs[0], mt.vs[1]);
-            if (__any_sync(0xffffffffu, move || vm > E_top)) {
-                float grow = 1.f;
-                if (vm > E_top) {
-                    const float top = __uint_as_float((__float_as_uint(vm) & 0x7f800000u) + 0x800000u);
-                    grow = E_top / top;
-                    E_top = top;
-                    E_inv = exp2_int(kPScale) / top;
-                }
+            if (__any_sync(0xffffffffu, move || fmaxf(mt.vs[0], mt.vs[1]) > vs_max)) {
+                // value scales are below 2^lv
+                const int lv0 = (int)(__float_as_uint(mt.vs[0]) >> 23) - 126;
+                const int lv1 = (int)(__float_as_uint(mt.vs[1]) >> 23) - 126;
+                float top = 0.f;
 #pragma unroll
                 for (int t = 0; t < kN; ++t) {
                     float al[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
-                                         fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mn = fmaxf(m[t][j], mx);
-                        al[j] = mn > m[t][j] ? exp2_approx(m[t][j] - mn) : 1.f;  // 0 from -inf
+                        float a0 = fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j];
+                        float a1 = fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, d));
+                            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, d));
+                        }
+                        const float mn = fmaxf(m[t][j], ceilf(fmaxf(a0, a1)));
+                        const int up = (int)fminf(mn - m[t][j], 300.f);  // 300 from -inf, and between infinities
+                        const bool had = pf[t][j] > 0.f;
+                        const int e_old = had ? kPScale + 127 - (int)(__float_as_uint(pf[t][j]) >> 23) - up : -1000;
+                        int e = max(e_old, (int)ceilf(fmaxf(a0 + (float)lv0, a1 + (float)lv1) - mn));
+                        e = min(max(max(e, max(lv0, lv1) - 110), kMinE), kMaxE);  // the step's factors stay finite
+                        const float was = exp2_int(max(-up, -127));               // 0 below 2^-126
+                        al[j] = exp2_int(max(e_old - e, -127));
+                        l[t][j] *= was;
                         m[t][j] = mn;
-                        l[t][j] *= al[j];
-                        al[j] *= grow;
+                        pf[t][j] = mn == -INFINITY ? 0.f : exp2_int(kPScale - e);
+                        top = fmaxf(top, pf[t][j]);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -779,23 +794,24 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                         o[t][j][3] *= al[1];
                     }
                 }
+                vs_max = kTopFactor * inverse_pow2(top);
             }
             // probabilities, their sums, and the second product
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const float cf = mt.vs[hf] * E_inv;
                 uint32_t ph[kN][2], pl_[kN][2];
 #pragma unroll
                 for (int t = 0; t < kN; ++t) {
                     const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                    const float c0 = mt.vs[hf] * pf[t][0], c1 = mt.vs[hf] * pf[t][1];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float p0 = exp2_approx(s[t][hf][2 * r] * f[t][hf][0] - m0);
                         float p1 = exp2_approx(s[t][hf][2 * r + 1] * f[t][hf][1] - m1);
                         l[t][0] += p0;
                         l[t][1] += p1;
-                        p0 *= cf;
-                        p1 *= cf;
+                        p0 *= c0;
+                        p1 *= c1;
                         const __half2 hi = __floats2half2_rn(p0, p1);
                         const float2 back = __half22float2(hi);
                         const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);

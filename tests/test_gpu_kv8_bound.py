@@ -85,3 +85,77 @@ def test_short_rows(kind, dtype, G, n_q, page):
     kc, table = _cache(lens, 2, page, kind, 5)
     q = _values(_gen(6), (len(lens), 2 * G, n_q, D)).to(dtype)
     assert _worst(q, kc, table, lens, G) <= 1
+
+
+def _pages_of_size(T, page, kind, dtype, G, n_q, bits):
+    """One row in which page i's scores lie bits[i][0] powers of two from zero
+    and its values bits[i][1] from 1.  Returns the cache, its table and q."""
+    g = _gen(7)
+    k, v, q = _values(g, (1, 2, T, D)), _values(g, (1, 2, T, D)), _values(g, (1, 2 * G, n_q, D)).to(dtype)
+    at = torch.arange(T, device=DEV) // page
+    score, size = (torch.tensor([b[i] for b in bits], device=DEV, dtype=torch.float32)[at] for i in (0, 1))
+    q[..., 0] = 4.0
+    k[..., 0] = score * (0.6931471805599453 * D ** 0.5 / 4.0)
+    v *= torch.exp2(size)[:, None]
+    kc = KV8Cache.empty(len(bits), 2, page, kind)
+    table = i32([random.Random(T).sample(range(len(bits)), len(bits))])
+    t = torch.arange(T, device=DEV)
+    ws = workspace(256)
+    spark_kv8_append(k, v, (table[0, t // page].long() * page + t % page).int()[None].contiguous(), kc, ws)
+    assert spark_device_status(ws) == 0
+    return kc, table, q
+
+
+def _worst_of_copies(q, kc, table, T, G, copies):
+    """One row `copies` times over the same pages: the teams of warps then take
+    stretches of many steps, which begin and end anywhere in the row."""
+    n_q = q.shape[2]
+    out = torch.full((copies,) + q.shape[1:], float("nan"), dtype=torch.float32, device=DEV)
+    ws = workspace(spark_workspace_bytes_kv8(copies, q.shape[1] // G, G, n_q))
+    spark_decode_attn_kv8(q.expand(copies, -1, -1, -1).contiguous(), kc, table.expand(copies, -1).contiguous(),
+                          i32([T] * copies), G, out, ws)
+    assert spark_device_status(ws) == 0
+    ref, tol = A.attention(q, kc.k, kc.v, kc.k_scale, kc.v_scale, kc.type, table, [T], [n_q], G, kc.page)
+    return max(A.worst(out[i:i + 1], ref, tol) for i in range(copies))
+
+
+FORMS = [(4, 1, torch.bfloat16), (4, 1, torch.float32), (8, 1, torch.bfloat16), (4, 4, torch.bfloat16),
+         (4, 4, torch.float32)]
+
+
+@pytest.mark.parametrize("copies", [1, 301])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n_q,dtype", FORMS)
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("where", [0, 5, 12])
+@pytest.mark.parametrize("R_", [12, 20, 28, 60])
+def test_a_page_of_large_values_without_weight(copies, kind, G, n_q, dtype, page, where, R_):
+    """Its value scale is 2^R times the others', its weight 2^-(R + 20)."""
+    bits = [(0, 0)] * 13
+    bits[where] = (-(R_ + 20), R_)
+    T = 13 * page - 3
+    kc, table, q = _pages_of_size(T, page, kind, dtype, G, n_q, bits)
+    assert _worst_of_copies(q, kc, table, T, G, copies) <= 1
+
+
+@pytest.mark.parametrize("copies", [1, 301])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n_q,dtype", FORMS)
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("step", [(3, -3), (-3, 3), (3, 2), (-2, -3), (0.25, 0), (5, -1)])
+def test_scores_and_values_that_climb_or_fall(copies, kind, G, n_q, dtype, page, step):
+    """Each page's scores and values lie some powers of two above or below those of the page before."""
+    bits = [(i * step[0] - 12 * step[0], i * step[1] - 12 * step[1]) for i in range(25)]
+    T = 25 * page - 5
+    kc, table, q = _pages_of_size(T, page, kind, dtype, G, n_q, bits)
+    assert _worst_of_copies(q, kc, table, T, G, copies) <= 1
+
+
+@pytest.mark.parametrize("copies", [1, 301])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n_q,dtype", FORMS)
+@pytest.mark.parametrize("size", [-116, -100, 100])
+def test_values_far_from_one(copies, kind, G, n_q, dtype, size):
+    T, page = 500, 32
+    kc, table, q = _pages_of_size(T, page, kind, dtype, G, n_q, [(0, size)] * 16)
+    assert _worst_of_copies(q, kc, table, T, G, copies) <= 1
