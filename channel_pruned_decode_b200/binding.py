@@ -41,7 +41,7 @@ EXPORTS = ("spark_lambda_to_T", "spark_cache_sizes", "spark_cache_bytes", "spark
            "spark_decode_attn_topp", "spark_topp_offsets_bytes", "spark_topp_vals_used",
            "spark_decode_attn_kv", "spark_workspace_bytes_kv", "spark_selftest_wait_timeout", "spark_tail_append", "spark_device_status",
            "spark_status_str", "spark_snapkv_evict", "spark_snapkv_evict_rows", "spark_pyramid_keep",
-           "spark_kv8_sizes", "spark_pages_extend", "spark_pages_trim", "spark_kv8_append",
+           "spark_kv8_sizes", "spark_pages_extend", "spark_pages_extend_served", "spark_pages_trim", "spark_kv8_append",
            "spark_decode_attn_kv8", "spark_workspace_bytes_kv8")
 
 
@@ -128,6 +128,8 @@ def lib():
         L.spark_kv8_sizes.restype = Z
         L.spark_pages_extend.argtypes = [P, P, I, I, P, I, P, P, I, I, P, P, P, P, Z, P]
         L.spark_pages_extend.restype = I
+        L.spark_pages_extend_served.argtypes = [P, P, I, I, P, I, P, P, I, I, P, P, P, P, P, Z, P]
+        L.spark_pages_extend_served.restype = I
         L.spark_pages_trim.argtypes = [P, P, I, I, P, I, P, P, I, P, P, P, Z, P]
         L.spark_pages_trim.restype = I
         L.spark_kv8_append.argtypes = [P, P, I, I, I, P, KV8, P, Z, P]
@@ -492,16 +494,21 @@ def spark_kv8_sizes(n_pages: int, Hkv: int, page: int, D: int = 128) -> tuple[in
 
 def spark_pages_extend(lens: torch.Tensor, n_new: torch.Tensor, page: int, pool: torch.Tensor, taken: torch.Tensor,
                        table: torch.Tensor, slots: torch.Tensor, lens_out: torch.Tensor, taken_out: torch.Tensor,
-                       ws: torch.Tensor, stream=None) -> None:
+                       ws: torch.Tensor, stream=None, n_served: torch.Tensor = None) -> None:
     """Pages for each row's n_new tokens (table [B, cap] and taken_out) and
-    their slots [B, n_cap]; lens_out / taken_out may be lens / taken."""
-    rc = _native().pages_extend(lens, n_new, page, pool, taken, table, slots, lens_out, taken_out, ws, _raw(stream))
+    their slots [B, n_cap]; lens_out / taken_out may be lens / taken.
+    n_served [B], an array of its own, gets the number of tokens that each row
+    got (fewer than n_new where the pool ran out): what the step's attention
+    takes as n_new (spark_pages_extend_served of include/spark.h)."""
+    rc = _native().pages_extend(lens, n_new, page, pool, taken, table, slots, lens_out, taken_out, ws, _raw(stream),
+                                n_served)
     if rc < 0:
         i32, B = torch.int32, lens.shape[0]
         _refuse("spark_pages_extend", ws, lens.device, ("lens", lens, i32, (B,)), ("n_new", n_new, i32, (B,)),
                 ("pool", pool, i32, (pool.numel(),)), ("taken", taken, i32, (1,)),
                 ("table", table, i32, (B, table.shape[-1])), ("slots", slots, i32, (B, slots.shape[-1])),
-                ("lens_out", lens_out, i32, (B,)), ("taken_out", taken_out, i32, (1,)))
+                ("lens_out", lens_out, i32, (B,)), ("taken_out", taken_out, i32, (1,)),
+                *([] if n_served is None else [("n_served", n_served, i32, (B,))]))
     if rc:
         _check(rc, "spark_pages_extend")
 

@@ -28,7 +28,8 @@ size_t snapkv_partials_bytes(long BH);
 
 cudaError_t launch_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
                                 int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
-                                int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *ws, cudaStream_t st);
+                                int32_t *slots, int32_t *lens_out, int32_t *taken_out, int32_t *n_served, void *ws,
+                                cudaStream_t st);
 cudaError_t launch_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool, int n_pages,
                               const int32_t *taken, const int32_t *table, int table_cap, int32_t *lens_out,
                               int32_t *taken_out, void *ws, cudaStream_t st);
@@ -441,9 +442,11 @@ static int check_pages(const int32_t *lens, const int32_t *n, int B, int page, c
     return SPARK_OK;
 }
 
-int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool, int n_pages,
-                       const int32_t *taken, int32_t *table, int table_cap, int n_cap, int32_t *slots,
-                       int32_t *lens_out, int32_t *taken_out, void *workspace, size_t ws_bytes, void *stream) {
+// n_served: NULL, or an array of its own
+static int pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool, int n_pages,
+                        const int32_t *taken, int32_t *table, int table_cap, int n_cap, int32_t *slots,
+                        int32_t *lens_out, int32_t *taken_out, int32_t *n_served, void *workspace, size_t ws_bytes,
+                        void *stream) {
     const int rc = check_pages(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, lens_out, taken_out);
     if (rc != SPARK_OK) return rc;
     if (n_cap < 0) return SPARK_ERR_ARG;
@@ -451,10 +454,31 @@ int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int pag
     if ((double)B * (n_cap / 2048 + 1) > 2147483647.0 || n_cap > (1 << 30)) return SPARK_ERR_UNSUPPORTED;
     if (B == 0) return SPARK_OK;
     if (n_cap > 0 && (!slots || !aligned16(slots))) return SPARK_ERR_ARG;
+    if (n_served) {
+        const size_t bytes = (size_t)B * 4;
+        for (const void *p : {(const void *)lens, (const void *)n_new, (const void *)lens_out})
+            if (p == n_served || overlap(p, n_served, bytes)) return SPARK_ERR_ARG;
+    }
     if (!workspace || !aligned16(workspace) || ws_bytes < (size_t)kWsHeader) return SPARK_ERR_WORKSPACE;
     cudaError_t e = launch_pages_extend(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, n_cap, slots,
-                                        lens_out, taken_out, workspace, static_cast<cudaStream_t>(stream));
+                                        lens_out, taken_out, n_served, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
+int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool, int n_pages,
+                       const int32_t *taken, int32_t *table, int table_cap, int n_cap, int32_t *slots,
+                       int32_t *lens_out, int32_t *taken_out, void *workspace, size_t ws_bytes, void *stream) {
+    return pages_extend(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, n_cap, slots, lens_out,
+                        taken_out, nullptr, workspace, ws_bytes, stream);
+}
+
+int spark_pages_extend_served(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
+                              int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
+                              int32_t *slots, int32_t *lens_out, int32_t *taken_out, int32_t *n_served,
+                              void *workspace, size_t ws_bytes, void *stream) {
+    if (B > 0 && (!n_served || !aligned4(n_served))) return SPARK_ERR_ARG;
+    return pages_extend(lens, n_new, B, page, pool, n_pages, taken, table, table_cap, n_cap, slots, lens_out,
+                        taken_out, n_served, workspace, ws_bytes, stream);
 }
 
 int spark_pages_trim(const int32_t *lens, const int32_t *keep, int B, int page, int32_t *pool, int n_pages,

@@ -68,19 +68,26 @@ int dtype_of(const at::Tensor *t) {
     return t->scalar_type() == at::kBFloat16 ? SPARK_BF16 : t->scalar_type() == at::kFloat ? SPARK_F32 : -1;
 }
 
-// lens, n_new, page, pool, taken, table, slots, lens_out, taken_out, ws, stream
+// lens, n_new, page, pool, taken, table, slots, lens_out, taken_out, ws, stream, n_served or None
 long pages_extend(PyObject *const *a) {
     const at::Tensor *lens = tensor(a[0]), *n_new = tensor(a[1]), *pool = tensor(a[3]), *taken = tensor(a[4]),
                      *table = tensor(a[5]), *slots = tensor(a[6]), *lens_out = tensor(a[7]),
-                     *taken_out = tensor(a[8]), *ws = tensor(a[9]);
+                     *taken_out = tensor(a[8]), *ws = tensor(a[9]),
+                     *served = a[11] == Py_None ? nullptr : tensor(a[11]);
     int page;
     void *st;
     if (!lens || !lens->is_cuda() || !small_int(a[2], &page)) return kRefused;
     const int64_t dev = lens->get_device(), B = lens->numel();
     if (lens->dim() != 1 || !row(lens, B, dev) || !row(n_new, B, dev) || !row(lens_out, B, dev) ||
         !matrix(table, B, dev) || !matrix(slots, B, dev) || !fits_int(pool, dev) || !row(taken, 1, dev) ||
-        !row(taken_out, 1, dev) || !ws || !fits(ws, ws->scalar_type(), dev) || !stream_of(a[10], dev, &st))
+        !row(taken_out, 1, dev) || (a[11] != Py_None && !row(served, B, dev)) || !ws ||
+        !fits(ws, ws->scalar_type(), dev) || !stream_of(a[10], dev, &st))
         return kRefused;
+    if (served)
+        return spark_pages_extend_served(ints(lens), ints(n_new), (int)B, page, ints(pool), (int)pool->numel(),
+                                         ints(taken), ints(table), (int)table->size(1), (int)slots->size(1),
+                                         ints(slots), ints(lens_out), ints(taken_out), ints(served), ws->data_ptr(),
+                                         ws->nbytes(), st);
     return spark_pages_extend(ints(lens), ints(n_new), (int)B, page, ints(pool), (int)pool->numel(), ints(taken),
                               ints(table), (int)table->size(1), (int)slots->size(1), ints(slots), ints(lens_out),
                               ints(taken_out), ws->data_ptr(), ws->nbytes(), st);
@@ -164,7 +171,7 @@ template <long (*kCall)(PyObject *const *), Py_ssize_t kArgs> PyMethodDef method
             nullptr};
 }
 
-PyMethodDef methods[] = {method<pages_extend, 11>("pages_extend"), method<pages_trim, 10>("pages_trim"),
+PyMethodDef methods[] = {method<pages_extend, 12>("pages_extend"), method<pages_trim, 10>("pages_trim"),
                          method<kv8_append, 7>("kv8_append"), method<decode_attn_kv8, 10>("decode_attn_kv8"),
                          {nullptr, nullptr, 0, nullptr}};
 

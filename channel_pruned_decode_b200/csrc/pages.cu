@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kPgThreads)
     pages_extend_kernel(const int32_t *lens, const int32_t *n_new, int B, int shift,
                         const int32_t *pool, int n_pages, const int32_t *taken, int32_t *table,
                         int table_cap, int n_cap, int32_t *slots, int32_t *lens_out,
-                        int32_t *taken_out, int chunks, int in_place, uint32_t *ws) {
+                        int32_t *taken_out, int32_t *n_served, int chunks, int in_place, uint32_t *ws) {
     __shared__ int sm[kPgThreads / 32];
     __shared__ int flag;
     const int b = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
@@ -155,13 +155,15 @@ __global__ void __launch_bounds__(kPgThreads)
     if (bad) atomicOr(ws, kDevBadArg);
     if (none && tid == 0) atomicOr(ws, kDevNoPages);
     // rows that the pool could not serve end with their last page
-    auto served = [&](const PageRow &x, int at, int want_x, int have_x) {
+    auto finish = [&](const PageRow &x, int i, int at, int want_x, int have_x) {
         const int got = have_x + max(0, min(want_x - have_x, n_pages - at));
-        return got < want_x ? max(x.len, min(x.len + x.n_new, got << shift)) : x.len + x.n_new;
+        const int end = got < want_x ? max(x.len, min(x.len + x.n_new, got << shift)) : x.len + x.n_new;
+        lens_out[i] = end;
+        if (n_served) n_served[i] = end - x.len;
     };
     if (!in_place) {
         if (chunk == 0 && tid == 0) {
-            lens_out[b] = served(r, base, want, have);
+            finish(r, b, base, want, have);
             if (b == B - 1) *taken_out = min(n_pages, base + (want - have));
         }
         return;
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kPgThreads)
         const int h = pages_of(x.len, shift), w = pages_of(x.len + x.n_new, shift);
         int total;
         const int pre = cta_scan(w - h, sm, &total);
-        if (i < B) lens_out[i] = served(x, at + pre, w, h);
+        if (i < B) finish(x, i, at + pre, w, h);
         at += total;
     }
     if (tid == 0) *taken_out = min(n_pages, at);
@@ -235,11 +237,12 @@ static int log2_page(int page) { return page == 16 ? 4 : page == 32 ? 5 : page =
 
 cudaError_t launch_pages_extend(const int32_t *lens, const int32_t *n_new, int B, int page, const int32_t *pool,
                                 int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
-                                int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *ws, cudaStream_t st) {
+                                int32_t *slots, int32_t *lens_out, int32_t *taken_out, int32_t *n_served, void *ws,
+                                cudaStream_t st) {
     const int chunks = n_cap > kPgSlots ? (n_cap + kPgSlots - 1) / kPgSlots : 1;
     return launch_after_prior(pages_extend_kernel, (unsigned)((long)B * chunks), kPgThreads, 0, st, lens, n_new, B,
                               log2_page(page), pool, n_pages, taken, table, table_cap, n_cap, slots, lens_out,
-                              taken_out, chunks, (int)(lens_out == lens || taken_out == taken),
+                              taken_out, n_served, chunks, (int)(lens_out == lens || taken_out == taken),
                               static_cast<uint32_t *>(ws));
 }
 

@@ -488,7 +488,10 @@ SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t s
  * Rows are served in order: row b's new pages are the next entries of the
  * pool.  When the pool runs out, the tokens without a page get slot -1, the
  * table entries without one get -1, lens_out counts only the tokens that
- * have one, and SPARK_ERR_PAGES is raised in the device status word.
+ * have one, and SPARK_ERR_PAGES is raised in the device status word.  A row
+ * then got fewer than n_new tokens: attention takes the number that it got
+ * (spark_pages_extend_served writes it), as with n_new it would place the
+ * row's queries too early.
  * Lengths out of range (negative, n_new > n_cap, more tokens than table_cap
  * pages hold, taken outside [0, n_pages], a page number outside the pool)
  * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
@@ -502,6 +505,21 @@ SPARK_API int spark_pages_extend(const int32_t *lens, const int32_t *n_new, int 
                                  int n_pages, const int32_t *taken, int32_t *table, int table_cap, int n_cap,
                                  int32_t *slots, int32_t *lens_out, int32_t *taken_out, void *workspace,
                                  size_t ws_bytes, void *stream);
+
+/*
+ * The same, which also writes how many of its new tokens each row got:
+ *   n_served  int32 [B], out: the row's length afterwards less the one before;
+ *             n_new[b] but where the pool ran out or n_new[b] was clamped.
+ *             An array of its own, apart from lens, n_new and lens_out.
+ * It is what spark_decode_attn_kv8 takes as n_new after this call: query i is
+ * then the row's i-th new token, and queries of tokens without a page are
+ * left as they are, without the host looking at the status word in between.
+ */
+SPARK_API int spark_pages_extend_served(const int32_t *lens, const int32_t *n_new, int B, int page,
+                                        const int32_t *pool, int n_pages, const int32_t *taken, int32_t *table,
+                                        int table_cap, int n_cap, int32_t *slots, int32_t *lens_out,
+                                        int32_t *taken_out, int32_t *n_served, void *workspace, size_t ws_bytes,
+                                        void *stream);
 
 /*
  * Cut rows to their first keep[b] tokens (0: the request has ended; keep >=
@@ -552,6 +570,8 @@ SPARK_API int spark_kv8_append(const void *k_new, const void *v_new, int B, int 
  *   n_new   int32 [B] or NULL          how many of the n_q queries row b has
  *                                      (NULL: all); query i is token
  *                                      lens[b] - n_new[b] + i of the row
+ *                                      (behind spark_pages_extend_served: its
+ *                                      n_served)
  *   out     [B][Hkv*G][n_q][D] fp32
  * Query i sees the tokens up to its own:
  *   out = softmax(q . K^T / sqrt(D)) V,  K, V = code * scale,
