@@ -117,20 +117,19 @@ __global__ void __launch_bounds__(kPgThreads)
     const int have = pages_of(r.len, shift), want = pages_of(r.len + r.n_new, shift);
     const int P = 1 << shift;
     int32_t *row = table + (size_t)b * table_cap;
-    // page number pg of the row: an old one from the table, a new one from the pool
+    bool bad = r.bad || *taken != tk, none = base + (want - have) > n_pages;
+    // page number pg of the row: an old one from the table, a new one from the
+    // pool; -1 and flagged where that is no page, -1 where the pool has run out
     auto page_at = [&](int pg) -> int {
         const int at = base + (pg - have);
         if (pg >= have && at >= n_pages) return -1;
         const int id = pg < have ? row[pg] : pool[at];
-        return id >= 0 && id < n_pages ? id : -1;
+        const bool ok = id >= 0 && id < n_pages;
+        bad |= !ok;
+        return ok ? id : -1;
     };
-    bool bad = r.bad || *taken != tk, none = base + (want - have) > n_pages;
     // this CTA's share of the row's new pages
-    for (int i = have + chunk * kPgThreads + tid; i < want; i += chunks * kPgThreads) {
-        const int id = page_at(i);
-        bad |= id < 0 && base + (i - have) < n_pages;
-        row[i] = id;
-    }
+    for (int i = have + chunk * kPgThreads + tid; i < want; i += chunks * kPgThreads) row[i] = page_at(i);
     // slots, four at a time where the row starts on 16 bytes
     const int j0 = chunk * kPgSlots, j1 = min(n_cap, j0 + kPgSlots);
     int32_t *srow = slots + (size_t)b * n_cap;

@@ -493,7 +493,8 @@ SPARK_API size_t spark_kv8_sizes(int n_pages, int Hkv, int page, int D, size_t s
  * (spark_pages_extend_served writes it), as with n_new it would place the
  * row's queries too early.
  * Lengths out of range (negative, n_new > n_cap, more tokens than table_cap
- * pages hold, taken outside [0, n_pages], a page number outside the pool)
+ * pages hold, taken outside [0, n_pages], a page number outside the pool
+ * where a new token goes, in the row's table or among the free pages)
  * are clamped, or their slots set to -1, and raise SPARK_ERR_ARG there.
  * Requires B * table_cap + n_pages < 2^31, table_cap * page < 2^31 and
  * n_pages * page < 2^31, n_cap <= 2^30 and B <= 65536.
