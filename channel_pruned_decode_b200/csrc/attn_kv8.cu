@@ -221,10 +221,13 @@ __device__ __forceinline__ int clamped_len(const AttnArgs &a, int b) {
     return min(max(a.lens[b], 0), a.table_cap * a.kc.page);
 }
 
+// 32-bit sums that pass a row's or the line's end (both below 2^31) are unsigned.
+__device__ __forceinline__ int steps_of(int len) { return (int)(((unsigned)len + (kStep - 1)) / kStep); }
+
 __device__ __forceinline__ void set_row(const AttnArgs &a, Place &p, int b) {
     p.b = b;
     p.len = clamped_len(a, b);
-    p.n_steps = (p.len + kStep - 1) / kStep;
+    p.n_steps = steps_of(p.len);
 }
 
 // The pair after p's (rows without tokens have no steps).
@@ -254,8 +257,8 @@ __device__ __forceinline__ void load_batch(const AttnArgs &a, const Place &p, in
     t.n = n;
     t.pg = -1;
     t.ks = t.vs = 0.f;
-    const int tok = p.s * kStep + lane * 16;
-    if (tok < p.len && lane < 2 * n) {
+    const unsigned tok = (unsigned)p.s * kStep + lane * 16;
+    if (tok < (unsigned)p.len && lane < 2 * n) {
         const int pg = a.table[(size_t)p.b * a.table_cap + (tok >> (31 - __clz(a.kc.page)))];
         if ((unsigned)pg < (unsigned)a.kc.n_pages) {
             t.pg = pg;
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             if (b < a.B) {
                 const int len = clamped_len(a, b), nn = a.n_new ? a.n_new[b] : a.n_q;
                 bad |= len != a.lens[b] || nn < 0 || nn > a.n_q;
-                mine += (len + kStep - 1) / kStep;
+                mine += steps_of(len);
             }
         }
         if (bad && blockIdx.x == 0) atomicOr(a.ws, kDevBadArg);
@@ -381,11 +384,11 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
         __syncthreads();
     }
     const int total = uniform(before[kAtThreads] * Hkv);
-    const int cta_share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinCtaSteps);
+    const int cta_share = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kMinCtaSteps);
     const int share = (cta_share + n_teams - 1) / n_teams;
     const int cta_from = (int)min((long long)blockIdx.x * cta_share, (long long)total);
     const int cta_steps = min(cta_share, total - cta_from);
-    const int from = cta_from + team * share;
+    const int from = (int)((unsigned)cta_from + team * share);  // past the line's end: no steps
     // teams without steps (and warps that make no whole team) only help to merge
     const int steps = team < n_teams ? max(0, min(share, cta_steps - team * share)) : 0;
     const int tm = blockIdx.x * n_teams + team;
@@ -690,7 +693,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             }
             // places without a token and tokens behind a query's own
             const bool holes = uniform(mt.nv[0] < 16 || mt.nv[1] < 16);
-            const bool edge = holes || t0 + kStep > first_full;
+            const bool edge = holes || t0 > first_full - kStep;
             bool hide = false;
             if (edge) {
 #pragma unroll
@@ -905,7 +908,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
     int pr[2] = {-1, -1}, qn[2] = {0, 0}, x0[2] = {0, 0}, x1[2] = {0, 0};  // the pairs, their queries, first and last step
     if (lane < n_teams && lane * share < cta_steps) {
         const Stretch x = stretch[lane];
-        const int f = cta_from + lane * share, t = min(f + share, cta_to);
+        const int f = cta_from + lane * share, t = f + min(share, cta_to - f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             pr[i] = x.pair[i];
