@@ -499,7 +499,9 @@ int spark_kv8_append(const void *k_new, const void *v_new, int B, int n_cap, int
     if (rc != SPARK_OK) return rc;
     if (B < 0 || n_cap < 0 || elem_size(dtype) == 0) return SPARK_ERR_ARG;
     // 32-bit counts of (row, page-sized piece, head, key or value) and of slots
-    if ((double)B * kc->Hkv * (n_cap / 16 + 2) * 2 > 2147483647.0 || (double)B * n_cap > 2147483647.0)
+    // (which pass n_cap by up to two pages)
+    if ((double)B * kc->Hkv * (n_cap / 16 + 2) * 2 > 2147483647.0 || (double)B * n_cap > 2147483647.0 ||
+        n_cap > (1 << 30))
         return SPARK_ERR_UNSUPPORTED;
     if ((long)B * kc->Hkv == 0 || n_cap == 0) return SPARK_OK;
     if (!k_new || !v_new || !slots || !aligned16(k_new) || !aligned16(v_new) || !aligned4(slots))

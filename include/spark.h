@@ -543,7 +543,8 @@ SPARK_API int spark_pages_trim(const int32_t *lens, const int32_t *keep, int B, 
  * Write new keys and values into their slots in 8 bits.
  *   k_new, v_new  [B][Hkv][n_cap][D] dtype (SPARK_F32 or SPARK_BF16)
  *   slots         int32 [B][n_cap] as written by spark_pages_extend; a
- *                 negative slot's token is not written
+ *                 negative slot's token is not written.  n_cap <= 2^30,
+ *                 B * n_cap < 2^31 and B * Hkv * (n_cap / 16 + 2) < 2^30
  * Per kv head, the new tokens that lie one after another in a page share a
  * scale: with a = their largest finite |x| and M = 448 (e4m3) or 127 (int8),
  * the scale is 2^E for the smallest E in [-126, 120] with a <= M 2^E.  Where
