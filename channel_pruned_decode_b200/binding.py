@@ -477,6 +477,10 @@ def _native():
         except ImportError as e:
             raise RuntimeError("the compiled binding (_calls.so) is missing or does not fit this Python; build it with "
                                "`python -m channel_pruned_decode_b200.build`") from e
+        from .build import calls_tag
+        if m.built_for != calls_tag():
+            raise RuntimeError(f"the compiled binding (_calls.so) was built for {m.built_for}, this is {calls_tag()}; "
+                               "build it again with `python -m channel_pruned_decode_b200.build`")
         _calls = m
     return _calls
 

@@ -12,6 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspark.so")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_TAG = os.path.join(PKG, "_build", "calls_tag")
 
 SOURCES = ["api.cu", "prune.cu", "decode.cu", "snapkv.cu", "think.cu", "pages.cu", "kv8.cu", "attn_kv8.cu"]
 NVCC_FLAGS = [
@@ -35,26 +36,49 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def calls_tag() -> str:
+    """What _calls.so is compiled for: it has torch's tensor accessors and
+    Python's object layout compiled in, so it fits this torch and Python only."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def calls_stale() -> bool:
+    """Whether _calls.so has to be compiled (again)."""
+    if _stale(CALLS, [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "spark.h"), LIB]):
+        return True
+    try:
+        with open(CALLS_TAG) as f:
+            return f.read() != calls_tag()
+    except OSError:
+        return True
+
+
 def build_calls(force: bool = False) -> str:
     """Compile csrc/calls.cpp, the native half of the binding of the paged
     8-bit cache's calls, into _calls.so beside libspark.so."""
+    if not force and not calls_stale():
+        return CALLS
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     src = os.path.join(CSRC, "calls.cpp")
-    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "spark.h"), LIB]):
-        return CALLS
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [INCLUDE, sysconfig.get_path("include"), cuda, *include_paths()]
-    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-Wall", "-Wextra",
+           f'-DSPARK_BUILT_FOR="{calls_tag()}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [x for i in includes for x in ("-isystem", i)] + [src, "-o", CALLS + ".tmp"]
     for d in library_paths():
         cmd += ["-L", d]
     cmd += ["-L", PKG, "-lspark", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     subprocess.run(cmd, check=True)
     os.replace(CALLS + ".tmp", CALLS)
+    os.makedirs(os.path.dirname(CALLS_TAG), exist_ok=True)
+    with open(CALLS_TAG, "w") as f:
+        f.write(calls_tag())
     return CALLS
 
 

@@ -175,8 +175,13 @@ PyMethodDef methods[] = {method<pages_extend, 12>("pages_extend"), method<pages_
                          method<kv8_append, 7>("kv8_append"), method<decode_attn_kv8, 10>("decode_attn_kv8"),
                          {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit__calls() { return PyModule_Create(&module_def); }
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit__calls() {
+    PyObject *m = PyModule_Create(&module_def);
+    // the binding refuses to use it under another torch or Python
+    if (m && PyModule_AddStringConstant(m, "built_for", SPARK_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}
