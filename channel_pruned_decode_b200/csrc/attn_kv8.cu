@@ -746,18 +746,23 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
             // need no maximum across lanes and no rescaling.  The same holds for E, the
             // reference of the products p * value scale: it is looked at where m moves,
             // and where a page's value scale alone might bring p out of fp16's range.
-            float f[kN][2][2];
             bool move = false;
 #pragma unroll
             for (int t = 0; t < kN; ++t)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    // above 0, so that an unseen place stays at -inf whatever its page's scale
-                    f[t][0][j] = fmaxf(qf[t][j] * mt.ks[0], exp2_int(-126));
-                    f[t][1][j] = fmaxf(qf[t][j] * mt.ks[1], exp2_int(-126));
-                    const float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j],
-                                           fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j]);
-                    move |= mx > m[t][j] + kSlack;
+                    // The scores are rounded here, once: fused into the subtraction below, a
+                    // product would lie up to half a step from the m that it gave, which
+                    // at scores from 2^27 on brings p out of fp16's range.
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        // above 0, so that an unseen place stays at -inf whatever its page's scale
+                        const float f = fmaxf(qf[t][j] * mt.ks[hf], exp2_int(-126));
+                        s[t][hf][j] = __fmul_rn(s[t][hf][j], f);
+                        s[t][hf][2 + j] = __fmul_rn(s[t][hf][2 + j], f);
+                    }
+                    const float mx = fmaxf(fmaxf(s[t][0][j], s[t][0][2 + j]), fmaxf(s[t][1][j], s[t][1][2 + j]));
+                    move |= mx - m[t][j] > kSlack;  // (m + kSlack may be rounded)
                 }
             if (__any_sync(0xffffffffu, move || fmaxf(mt.vs[0], mt.vs[1]) > vs_max)) {
                 // value scales are below 2^lv
@@ -769,8 +774,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     float al[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float a0 = fmaxf(s[t][0][j], s[t][0][2 + j]) * f[t][0][j];
-                        float a1 = fmaxf(s[t][1][j], s[t][1][2 + j]) * f[t][1][j];
+                        float a0 = fmaxf(s[t][0][j], s[t][0][2 + j]), a1 = fmaxf(s[t][1][j], s[t][1][2 + j]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) {
                             a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, d));
@@ -780,7 +784,7 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                         const int up = (int)fminf(mn - m[t][j], 300.f);  // 300 from -inf, and between infinities
                         const bool had = pf[t][j] > 0.f;
                         const int e_old = had ? kPScale + 127 - (int)(__float_as_uint(pf[t][j]) >> 23) - up : -1000;
-                        int e = max(e_old, (int)ceilf(fmaxf(a0 + (float)lv0, a1 + (float)lv1) - mn));
+                        int e = max(e_old, (int)ceilf(fmaxf(a0 - mn + (float)lv0, a1 - mn + (float)lv1)));
                         e = min(max(max(e, max(lv0, lv1) - 110), kMinE), kMaxE);  // the step's factors stay finite
                         const float was = exp2_int(max(-up, -127));               // 0 below 2^-126
                         al[j] = exp2_int(max(e_old - e, -127));
@@ -809,8 +813,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                     const float c0 = mt.vs[hf] * pf[t][0], c1 = mt.vs[hf] * pf[t][1];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float p0 = exp2_approx(s[t][hf][2 * r] * f[t][hf][0] - m0);
-                        float p1 = exp2_approx(s[t][hf][2 * r + 1] * f[t][hf][1] - m1);
+                        float p0 = exp2_approx(s[t][hf][2 * r] - m0);
+                        float p1 = exp2_approx(s[t][hf][2 * r + 1] - m1);
                         l[t][0] += p0;
                         l[t][1] += p1;
                         p0 *= c0;

@@ -1,5 +1,6 @@
 """Attention over the paged 8-bit cache held to the bound of
 tests/_kv8_bound.py, which is relative to sum p |v| of each channel."""
+import math
 import random
 
 import pytest
@@ -159,3 +160,37 @@ def test_values_far_from_one(copies, kind, G, n_q, dtype, size):
     T, page = 500, 32
     kc, table, q = _pages_of_size(T, page, kind, dtype, G, n_q, [(0, size)] * 16)
     assert _worst_of_copies(q, kc, table, T, G, copies) <= 1
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n_q,dtype", FORMS)
+@pytest.mark.parametrize("top", [3, 250, 399])
+@pytest.mark.parametrize("a", [10, 24, 26, 27, 28, 31, 40, 100])
+def test_scores_far_beyond_the_steps_of_fp32(kind, G, n_q, dtype, top, a):
+    """Scores of 2^a / sqrt(128) times 0 .. 8: the softmax is the one token with
+    8, whatever its page's value scale and where the scores' reference stood."""
+    T, page, H = 400, 16, 2
+    g = _gen(9)
+    k, v = torch.zeros((1, H, T, D), device=DEV), _values(g, (1, H, T, D))
+    k[..., 0] = torch.randint(0, 8, (1, H, T), generator=g, device=DEV).float()
+    k[..., top, 0] = 8.0
+    v *= torch.exp2(torch.randint(-20, 21, (T // page,), generator=g, device=DEV).float()).repeat_interleave(page)[:, None]
+    q = torch.zeros((1, H * G, n_q, D), device=DEV)
+    q[..., 0] = 2.0 ** a
+    kc = KV8Cache.empty(T // page, H, page, kind)
+    table, ws = torch.arange(T // page, dtype=torch.int32, device=DEV)[None], workspace(256)
+    spark_kv8_append(k, v, torch.arange(T, dtype=torch.int32, device=DEV)[None], kc, ws)
+    copies = 301
+    out = torch.full((copies, H * G, n_q, D), float("nan"), dtype=torch.float32, device=DEV)
+    wsa = workspace(spark_workspace_bytes_kv8(copies, H, G, n_q))
+    spark_decode_attn_kv8(q.to(dtype).expand(copies, -1, -1, -1).contiguous(), kc,
+                          table.expand(copies, -1).contiguous(), i32([T] * copies), G, out, wsa)
+    assert spark_device_status(wsa) == 0
+    for h in range(H):
+        want = R.decode(kc.v[top // page, h, top % page], kind) * kc.v_scale[top // page, h].double()
+        sees = torch.tensor([top <= T - n_q + i for i in range(n_q)], device=DEV)
+        got = out[:, h * G:(h + 1) * G][:, :, sees].double()
+        # p is 1, its halves keep 22 bits, and a merge and the division round once
+        # each; the other tokens weigh at most exp(-2^a / sqrt(128)) each
+        room = 2.0 ** -20 * want.abs() + T * float(v.abs().max()) * 2 * math.exp(-min(700.0, 2.0 ** a / D ** 0.5))
+        assert bool(((got - want).abs() <= room).all())
