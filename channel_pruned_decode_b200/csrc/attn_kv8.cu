@@ -37,8 +37,8 @@
 // (about 23 bytes a clock and SM, 90 % of the copy rate between the first
 // stage's arrival and the last step), with 2.6 us before it (lengths, their
 // sum, table, pages: four dependent reads) and 4 to 8 us behind it (slowest
-// SM, merges).  At 16 rows by dependent-issue latency: 255 registers leave 8
-// warps, issue slots are 35 % used, and 75 to 77 us of 4 verified tokens compare
+// SM, merges).  At 16 rows by dependent-issue latency: some 250 registers leave 8
+// warps, issue slots are 35 % used, and 77 us of 4 verified tokens compare
 // with 41 us of memory time.
 #include <cuda.h>  // CUtensorMap and its enums (the encoder is fetched at run time)
 
@@ -109,8 +109,8 @@ __device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu,
 
 // The same value, of which the compiler knows nothing.  Conditions on launch
 // constants inside the main loop go through this: the compiler would make a
-// copy of the whole loop for each outcome of each of them (110 KB of code
-// instead of 19), and what a CTA runs once costs what its fetch costs.
+// copy of the whole loop for each outcome of each of them, and what a CTA runs
+// once costs what its fetch costs.
 __device__ __forceinline__ int opaque(int x) {
     asm volatile("" : "+r"(x));
     return x;
@@ -209,7 +209,7 @@ struct Place {
 struct AttnArgs {
     spark_kv8cache kc;
     const int32_t *table, *lens, *n_new;
-    int table_cap, B, rows, G, n_q, team_warps, n_stages;
+    int table_cap, B, rows, n_q, team_warps, n_stages;
     float *out;
     uint32_t *ws, *counter;
     float4 *flush;          // flushed sums
@@ -1102,7 +1102,6 @@ cudaError_t launch_attn_kv8(const void *q, int dtype, const spark_kv8cache &kc, 
     a.table_cap = table_cap;
     a.B = B;
     a.rows = G * n_q;
-    a.G = G;
     a.n_q = n_q;
     a.out = out;
     char *w = static_cast<char *>(ws);

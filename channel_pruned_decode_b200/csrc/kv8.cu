@@ -294,10 +294,9 @@ static cudaError_t launch_append(const E *k_new, const E *v_new, int B, int n_ca
     const int teams = kWarps / (kc.page / ApGeom<E>::kTokens);
     // Where the GPU is full more than once, a team takes the keys and the values
     // of a head, which share its look at the slots.  32 x
-    // 2048 tokens of 8 heads in bf16: 1 at a time 77.7 us, 2 70.1, 4 71.4, 8 75.4,
-    // 16 77.0; 5 x 1777 tokens of 4 heads in fp32: 14.4, 13.6, 16.1, 24.6 (the GPU
-    // no longer full).  That was before later steps: 2 at a time now takes 63 to
-    // 66 us and 10.4, the others were not measured again.
+    // 2048 tokens of 8 heads in bf16: 1 at a time 68.7 us, 2 63.0, 4 66.0, 8 67.5,
+    // 16 72.3; 5 x 1777 tokens of 4 heads in fp32: 11.4, 9.6, 14.5, 23.5 (the GPU
+    // no longer full).
     const long warps = (long)B * pieces * kc.Hkv * 2 * (kWarps / teams);
     const int per = warps > 32l * num_sms ? 2 : 1;
     const long units = (long)B * pieces * ((2 * kc.Hkv + per - 1) / per);

@@ -10,9 +10,12 @@
 //           behind it go back to pool[taken - total + (pages of rows before)].
 // Both are a prefix sum over the rows and a copy.  Each CTA sums the rows
 // before its own itself (a few loads a thread, from L2), which costs less than
-// a second launch for the sum at serving batches; the work grows with B^2 (one
-// token a row: 4 us for 512 rows, 13 for 4096, 95 for 16384, 1.2 ms for 65536, the
-// most a call takes; trim 3, 14, 162, 2.4 ms).  lens_out may be lens and taken_out may be
+// a second launch for the sum at serving batches.  The work grows with B^2, and
+// extend's with the 2048-slot pieces of a row too, each a CTA that sums anew:
+// one token a row takes 6 us for 512 rows (each without a page before), 14 for
+// 4096, 94 for 16384, 1.2 ms for 65536, the most a call takes (trim 5, 15, 163,
+// 2.4 ms); 8192 tokens a row 10 us for 512 rows, 71 for 4096 (their slots alone
+// 21), 471 for 16384 (82), 5.1 ms for 65536 (329).  lens_out may be lens and taken_out may be
 // taken (a replayed graph advances them in place): they are then written by
 // the last CTA to finish, when every other one has read them.
 //
