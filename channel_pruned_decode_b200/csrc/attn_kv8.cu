@@ -18,8 +18,8 @@
 // fp16 halves (22 bits).  P is multiplied by the page's value scale and 2^6
 // over a power of two that follows the row's largest product of the two, and
 // enters as two fp16 halves: 22 bits, down to 2^-29 of that product, however
-// far the value scales of a row lie apart (up to 2^110).  The sums come out with
-// the error of fp32 ones.  The codes of values are paired by token with byte permutes
+// far the value scales of a row lie apart.  The sums come out with the error of
+// fp32 ones.  The codes of values are paired by token with byte permutes
 // in registers (the transpose that the second product needs), P is transposed
 // by movmatrix; nothing else crosses lanes but the row maxima.
 //
@@ -785,8 +785,8 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
                         const bool had = pf[t][j] > 0.f;
                         const int e_old = had ? kPScale + 127 - (int)(__float_as_uint(pf[t][j]) >> 23) - up : -1000;
                         int e = max(e_old, (int)ceilf(fmaxf(a0 - mn + (float)lv0, a1 - mn + (float)lv1)));
-                        e = min(max(max(e, max(lv0, lv1) - 110), kMinE), kMaxE);  // the step's factors stay finite
-                        const float was = exp2_int(max(-up, -127));               // 0 below 2^-126
+                        e = min(max(e, kMinE), kMaxE);
+                        const float was = exp2_int(max(-up, -127));  // 0 below 2^-126
                         al[j] = exp2_int(max(e_old - e, -127));
                         l[t][j] *= was;
                         m[t][j] = mn;
@@ -810,15 +810,14 @@ __global__ void __launch_bounds__(AtGeom<kNT>::kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < kN; ++t) {
                     const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-                    const float c0 = mt.vs[hf] * pf[t][0], c1 = mt.vs[hf] * pf[t][1];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float p0 = exp2_approx(s[t][hf][2 * r] - m0);
                         float p1 = exp2_approx(s[t][hf][2 * r + 1] - m1);
                         l[t][0] += p0;
                         l[t][1] += p1;
-                        p0 *= c0;
-                        p1 *= c1;
+                        p0 = p0 * mt.vs[hf] * pf[t][0];  // in this order: the two factors may be far apart
+                        p1 = p1 * mt.vs[hf] * pf[t][1];
                         const __half2 hi = __floats2half2_rn(p0, p1);
                         const float2 back = __half22float2(hi);
                         const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);

@@ -578,8 +578,8 @@ SPARK_API int spark_kv8_append(const void *k_new, const void *v_new, int B, int 
  * Query i sees the tokens up to its own:
  *   out = softmax(q . K^T / sqrt(D)) V,  K, V = code * scale,
  * with fp32 products' sums and statistics: the error is that of fp32 sums,
- * relative to sum p |v| of each channel, where the value scales of a row lie
- * within 2^110 of one another.  A query that sees no token gets
+ * relative to sum p |v| of each channel, however far the scales of a row lie
+ * apart (a p below 2^-126 counts as 0).  A query that sees no token gets
  * zeros, and the rows of queries i >= n_new[b] are left as they are.  What
  * the pages hold past lens[b], and table entries past it, is never used.
  * Requires 1 <= G * n_q <= 64, finite scales that are not negative, and

@@ -194,3 +194,16 @@ def test_scores_far_beyond_the_steps_of_fp32(kind, G, n_q, dtype, top, a):
         # each; the other tokens weigh at most exp(-2^a / sqrt(128)) each
         room = 2.0 ** -20 * want.abs() + T * float(v.abs().max()) * 2 * math.exp(-min(700.0, 2.0 ** a / D ** 0.5))
         assert bool(((got - want).abs() <= room).all())
+
+
+@pytest.mark.parametrize("copies", [1, 301])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n_q,dtype", FORMS)
+@pytest.mark.parametrize("where", [0, 5, 12])
+def test_value_scales_at_both_ends_of_their_range(copies, kind, G, n_q, dtype, where):
+    """A page whose value scale is 2^200 times the others' and whose weight is 2^-240."""
+    bits = [(0, -100)] * 13
+    bits[where] = (-240, 100)
+    T, page = 13 * 16 - 3, 16
+    kc, table, q = _pages_of_size(T, page, kind, dtype, G, n_q, bits)
+    assert _worst_of_copies(q, kc, table, T, G, copies) <= 1
